@@ -117,7 +117,8 @@ enum {
   SV_S_Q_UNAVAILABLE = -3, /* rule 2 and draft_logits == NULL (sdcp-q-unavailable) */
   SV_S_BAD_PROPOSAL = -1,  /* a token outside [0, V); or, after the logits check,
                               q_i(x_i) == 0 for some i <= m[b] (sdcp-bad-proposal) */
-  SV_S_BAD_LOGITS = -5     /* NaN / +inf, or no finite logit, in a row the rule reads */
+  SV_S_BAD_LOGITS = -5,    /* NaN / +inf, or no finite logit, in a row the rule reads */
+  SV_S_BAD_CONTROL = -6    /* sv_adjust_logits only: penalties, slot, bias or mask out of range */
 };
 
 /* Bytes of device workspace sv_verify needs for (B, M, V).  0 if the sizes
@@ -376,6 +377,169 @@ int sv_verify_noalloc(const void *target_logits, const void *draft_logits, int32
                       const sv_sampling *sampling, int32_t B, int32_t M, int32_t V, uint64_t seed,
                       uint32_t round, int32_t *accepted_len, int32_t *out_tokens,
                       const sv_probe *probe, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Per-session rules on logits: what a serving sampler does to the target's (and
+ * the drafter's) logits before the acceptance step, and the state those rules
+ * keep.  A round with all of them:
+ *   sv_grammar_advance  states before every row, from the drafted tokens
+ *   sv_adjust_logits    penalties, biases and masks on the rows
+ *   sv_verify ...       the acceptance step on the adjusted rows
+ *   sv_commit           (or sv_verify_commit for both)
+ *   sv_count_tokens     the committed tokens into the history
+ *   sv_grammar_advance  states after the committed tokens
+ * Bit rows over the vocabulary hold token v in bit v % 32 of word v / 32 and
+ * are W = (V + 31) / 32 words long; bits at and past V are ignored when read
+ * and written as zeros.  Every call only enqueues work on stream, allocates
+ * nothing and keeps no pointer; the host structs are read before it returns.
+ * ------------------------------------------------------------------------- */
+
+/* Per-session penalties for repeated tokens, 16 bytes; a DEVICE array [B]. */
+typedef struct sv_penalties {
+  float repetition;  /* finite and > 0; 1 = off */
+  float frequency;   /* finite; 0 = off */
+  float presence;    /* finite; 0 = off */
+  uint32_t reserved; /* must be 0 */
+} sv_penalties;
+
+/* Which tokens each session has had: a pool of n_slots slots (a HOST struct of
+ * DEVICE pointers).  seen[h][0] has the bits of the prompt's tokens, seen[h][1]
+ * those of the output tokens, counts[h][v] how often v was output; a token's
+ * output bit is set exactly where its count is not 0 (counts of other tokens
+ * are not read).  sv_count_tokens keeps all three. */
+typedef struct sv_history {
+  int32_t *counts; /* [n_slots, V] */
+  uint32_t *seen;  /* [n_slots, 2, W] */
+  int32_t n_slots;
+} sv_history;
+
+/* Sparse biases: session b has entries offsets[b] .. offsets[b+1]-1 of ids
+ * (strictly ascending within a session; ids outside [0, V) have no effect) and
+ * values.  A HOST struct of DEVICE pointers. */
+typedef struct sv_bias {
+  const int32_t *offsets; /* [B + 1] */
+  const int32_t *ids;     /* [n] */
+  const float *values;    /* [n] */
+  int32_t n;
+} sv_bias;
+
+/* Vocabulary masks: bit 1 = allowed.  rows[b][r] is the mask of session b's
+ * row r, or -1 for none.  A HOST struct of DEVICE pointers. */
+typedef struct sv_masks {
+  const uint32_t *bits; /* [n_masks, W] */
+  const int32_t *rows;  /* [B, R] */
+  int32_t n_masks;
+} sv_masks;
+
+/*
+ * Penalties, biases and masks on a round's logits.  Row r (0-based) of session
+ * b scores the position after its drafted tokens x_1..x_r.  R == M + 1: target
+ * rows, of which a session uses m[b] + 1; R == M: draft rows, m[b] of them; M
+ * == 0 and R == 1: a decoding step.  For each token v of a used row, in
+ * binary32:
+ *   c = counts[h][v] (h = the session's slot) + how often v is in x_1..x_r
+ *   z = logit;  if v is in the prompt or c > 0:  z = z > 0 ? z / repetition
+ *                                                          : z * repetition
+ *   z = z - frequency * c - (c > 0 ? presence : 0) + bias(v)
+ *   z = -inf where the row's mask has bit 0, whatever it was
+ * rounded once to dtype; tokens that no rule changes keep their bits.  Rows a
+ * session does not use are neither read nor written.  A mask that allows
+ * nothing leaves a row of -inf, which the acceptance step reports as
+ * SV_S_BAD_LOGITS.
+ *   logits  DEVICE, of dtype: row r of session b starts at element b *
+ *           session_stride + r * row_stride (both >= 0), its V logits are
+ *           contiguous;
+ *   out     DEVICE [B, R, V] contiguous, not overlapping logits; or logits
+ *           itself (in place: only logits that change are written, and the
+ *           strides must keep the used rows apart);
+ *   draft_tokens [B, M] int32 (NULL only if M == 0 or penalties == NULL), m
+ *           [B] int32 with 0 <= m[b] <= M, or NULL for m[b] = M;
+ *   penalties [B], history, bias, masks: each may be NULL (that rule is off);
+ *           history only acts with penalties, without it c counts the drafted
+ *           tokens alone;
+ *   slots   [B] int32: session b's slot of history, -1 for none; NULL: slot b;
+ *   status  [B] int32 or NULL: 0, or why session b failed, checked in this
+ *           order: SV_S_LIMIT (m[b]), SV_S_BAD_CONTROL (penalties, slot, bias
+ *           offsets or a used row's mask out of range), SV_S_BAD_PROPOSAL (a
+ *           token of x_1..x_m outside [0, V), with penalties).  All R rows of a
+ *           failed session become NaN, so that nothing is sampled from them.
+ * Sizes: 1 <= B <= SV_B_MAX, 0 <= M <= 64, 1 <= R, 1 <= V <= SV_V_MAX.
+ * A row's result depends only on its session's arguments.  Returns SV_OK,
+ * SV_ERR_ARG or SV_ERR_DEVICE.
+ */
+int sv_adjust_logits(const void *logits, int64_t session_stride, int64_t row_stride, int32_t dtype,
+                     const int32_t *draft_tokens, const int32_t *m, const sv_penalties *penalties,
+                     const sv_history *history, const int32_t *slots, const sv_bias *bias,
+                     const sv_masks *masks, int32_t B, int32_t M, int32_t R, int32_t V, void *out,
+                     int32_t *status, void *stream);
+
+/*
+ * Notes tokens in the history.  Session b's tokens are tokens[b * L] ..
+ * tokens[b * L + n - 1] with n = lens[b] (NULL: L) cut to [0, L], or, with
+ * offsets (DEVICE [B + 1], ascending; lens must be NULL and L = the length of
+ * tokens), tokens[offsets[b]] .. tokens[offsets[b+1] - 1] (cut to [0, L)).
+ * Tokens outside [0, V), such as the -1 that ends out_tokens, are skipped.
+ * plane 0: prompt tokens, their prompt bits are set; plane 1: output tokens,
+ * their counts grow and their output bits are set.  clear != 0: the listed
+ * slots are first emptied (counts and both planes).  slots [B] int32, or NULL
+ * for slot b; a session whose slot is outside [0, n_slots) is skipped.  Several
+ * sessions may name the same slot: their tokens add up.  Whole-number updates:
+ * the result does not depend on their order.  After the commit step: tokens =
+ * out_tokens, L = M + 1, lens = emitted_len, plane = 1.
+ * 1 <= B <= SV_B_MAX, 0 <= L, 1 <= V <= SV_V_MAX.  Calls that overlap on the
+ * same slots race.  Returns SV_OK, SV_ERR_ARG or SV_ERR_DEVICE.
+ */
+int sv_count_tokens(const sv_history *history, const int32_t *slots, const int32_t *tokens,
+                    const int32_t *offsets, const int32_t *lens, int32_t B, int32_t L, int32_t V,
+                    int32_t plane, int32_t clear, void *stream);
+
+/* A byte automaton: from state s a byte c leads to next[s][classes[c]], or is
+ * refused where that is outside [0, n_states) (-1 by custom).  One table may
+ * hold several grammars, each with its own start state.  A HOST struct of
+ * DEVICE pointers. */
+typedef struct sv_grammar {
+  const int32_t *next;    /* [n_states, n_classes] */
+  const uint8_t *classes; /* [256]; a class >= n_classes is refused everywhere */
+  const uint8_t *accept;  /* [n_states]: not 0 where a text may end */
+  int32_t n_states;       /* >= 1 */
+  int32_t n_classes;      /* 1..256 */
+} sv_grammar;
+
+/* The tokens' bytes: token v's are bytes[offsets[v]] .. bytes[offsets[v+1]-1];
+ * none for control tokens.  end: up to SV_STOP_MAX tokens that end a text
+ * (their bytes, if any, do not count).  A HOST struct of DEVICE pointers. */
+typedef struct sv_vocab {
+  const uint8_t *bytes;   /* [n_bytes] */
+  const int32_t *offsets; /* [V + 1], ascending, within [0, n_bytes] */
+  const int32_t *end;     /* [n_end] */
+  int32_t n_bytes, n_end, V;
+} sv_vocab;
+
+/*
+ * The masks of n automaton states: bits [n, W] uint32, row k for states[k].  In
+ * a state of the automaton a token is allowed if it has bytes and none of them
+ * is refused, an end token if the state accepts, another token without bytes
+ * never.  For states outside [0, n_states) (-1: no grammar) every token is
+ * allowed.  Returns SV_OK, SV_ERR_ARG (also n < 1) or SV_ERR_DEVICE.
+ */
+int sv_grammar_masks(const sv_grammar *grammar, const sv_vocab *vocab, const int32_t *states,
+                     int32_t n, uint32_t *bits, void *stream);
+
+/*
+ * Automaton states along tokens: out_states [B, L + 1], out_states[b][i] the
+ * state after the first i tokens of session b, which starts in states[b].  It
+ * is -1 (no grammar) from the start where states[b] is outside [0, n_states),
+ * after a token that is not allowed or ends the text, and for i > lens[b].  A
+ * round's row r takes the mask of out_states[b][r]: a drafted token that is not
+ * allowed has probability zero in its own row, so its position rejects and the
+ * rows after it, which carry no mask, do not count.  tokens [B, L] int32, lens
+ * [B] (cut to [0, L]) or NULL for L.  last [B] or NULL: the state after all
+ * lens[b] tokens; last may be states.  1 <= B <= SV_B_MAX, 0 <= L <= 65.
+ * Returns SV_OK, SV_ERR_ARG or SV_ERR_DEVICE.
+ */
+int sv_grammar_advance(const sv_grammar *grammar, const sv_vocab *vocab, const int32_t *states,
+                       const int32_t *tokens, const int32_t *lens, int32_t B, int32_t L,
+                       int32_t *out_states, int32_t *last, void *stream);
 
 /* Benchmark hook, not part of the acceptance step: hipEvent_t handles that
  * the sv_verify* calls made afterwards from the calling host thread record on

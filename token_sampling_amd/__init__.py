@@ -14,8 +14,10 @@ Rule 2 speculative sampling).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -36,6 +38,7 @@ S_LIMIT = -2
 S_Q_UNAVAILABLE = -3
 S_BAD_PROFILE = -4
 S_BAD_LOGITS = -5
+S_BAD_CONTROL = -6  # adjust_logits: penalties, slot, bias offsets or mask row out of range
 
 SAMPLING_DTYPE = np.dtype(
     [("temperature_milli", "<u4"), ("top_k", "<u4"), ("top_p_milli", "<u4"),
@@ -64,7 +67,11 @@ STATE_DTYPE = np.dtype(
 EXPORTED = ("sv_workspace_bytes", "sv_verify", "sv_verify_sdcp", "sv_verify_qrows",
             "sv_verify_early", "sv_commit",
             "sv_prefix_digest", "sv_contract_digest", "sv_strerror", "sv_status_str",
-            "sv_version", "sv_bench_row_events", "sv_verify_noalloc", "sv_verify_commit")
+            "sv_version", "sv_bench_row_events", "sv_verify_noalloc", "sv_verify_commit",
+            "sv_adjust_logits", "sv_count_tokens", "sv_grammar_masks", "sv_grammar_advance")
+# Per-session penalties for repeated tokens (sv_penalties, 16 bytes).
+PENALTIES_DTYPE = np.dtype([("repetition", "<f4"), ("frequency", "<f4"), ("presence", "<f4"),
+                            ("reserved", "<u4")], align=True)
 
 
 class SvError(RuntimeError):
@@ -79,6 +86,63 @@ class _CommitIO(ctypes.Structure):
     _fields_ = [("contracts", ctypes.c_void_p), ("states", ctypes.c_void_p),
                 ("self_decode_ok", ctypes.c_void_p), ("emitted_len", ctypes.c_void_p),
                 ("action", ctypes.c_void_p)]
+
+
+class _History(ctypes.Structure):
+    _fields_ = [("counts", ctypes.c_void_p), ("seen", ctypes.c_void_p), ("n_slots", ctypes.c_int32)]
+
+
+class _Bias(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("ids", ctypes.c_void_p), ("values", ctypes.c_void_p),
+                ("n", ctypes.c_int32)]
+
+
+class _Masks(ctypes.Structure):
+    _fields_ = [("bits", ctypes.c_void_p), ("rows", ctypes.c_void_p), ("n_masks", ctypes.c_int32)]
+
+
+class _Grammar(ctypes.Structure):
+    _fields_ = [("next", ctypes.c_void_p), ("classes", ctypes.c_void_p),
+                ("accept", ctypes.c_void_p), ("n_states", ctypes.c_int32),
+                ("n_classes", ctypes.c_int32)]
+
+
+class _Vocab(ctypes.Structure):
+    _fields_ = [("bytes", ctypes.c_void_p), ("offsets", ctypes.c_void_p), ("end", ctypes.c_void_p),
+                ("n_bytes", ctypes.c_int32), ("n_end", ctypes.c_int32), ("V", ctypes.c_int32)]
+
+
+class History(NamedTuple):
+    """Which tokens each slot has had (sv_history): counts [n_slots, V] int32 of
+    the output tokens, seen [n_slots, 2, W] int32 bit rows over the vocabulary, W
+    = (V + 31) // 32 (plane 0: prompt, plane 1: output).  See make_history."""
+    counts: "torch.Tensor"  # noqa: F821
+    seen: "torch.Tensor"  # noqa: F821
+
+
+class Bias(NamedTuple):
+    """Sparse biases (sv_bias): session b's entries are offsets[b]..offsets[b+1]-1
+    of ids (int32, strictly ascending within a session) and values (float32).
+    See make_bias."""
+    offsets: "torch.Tensor"  # noqa: F821
+    ids: "torch.Tensor"  # noqa: F821
+    values: "torch.Tensor"  # noqa: F821
+
+
+class Grammar(NamedTuple):
+    """A byte automaton (sv_grammar): next [n_states, n_classes] int32 (-1:
+    refused), classes [256] uint8, accept [n_states] uint8.  See make_grammar."""
+    next: "torch.Tensor"  # noqa: F821
+    classes: "torch.Tensor"  # noqa: F821
+    accept: "torch.Tensor"  # noqa: F821
+
+
+class Vocab(NamedTuple):
+    """The tokens' bytes (sv_vocab): bytes uint8, offsets [V + 1] int32, end: up to
+    8 int32 ids of the tokens that end a text.  See make_vocab."""
+    bytes: "torch.Tensor"  # noqa: F821
+    offsets: "torch.Tensor"  # noqa: F821
+    end: "torch.Tensor"  # noqa: F821
 
 
 class HipEvent:
@@ -190,6 +254,16 @@ def lib():
             ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(_Probe), ctypes.c_void_p,
         ]
         L.sv_verify_commit.restype = ctypes.c_int
+        p, i = ctypes.c_void_p, ctypes.c_int32
+        L.sv_adjust_logits.argtypes = [
+            p, ctypes.c_int64, ctypes.c_int64, i, p, p, p, ctypes.POINTER(_History), p,
+            ctypes.POINTER(_Bias), ctypes.POINTER(_Masks), i, i, i, i, p, p, p]
+        L.sv_count_tokens.argtypes = [ctypes.POINTER(_History), p, p, p, p, i, i, i, i, i, p]
+        L.sv_grammar_masks.argtypes = [ctypes.POINTER(_Grammar), ctypes.POINTER(_Vocab), p, i, p, p]
+        L.sv_grammar_advance.argtypes = [ctypes.POINTER(_Grammar), ctypes.POINTER(_Vocab), p, p, p,
+                                         i, i, p, p, p]
+        for f in (L.sv_adjust_logits, L.sv_count_tokens, L.sv_grammar_masks, L.sv_grammar_advance):
+            f.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -488,3 +562,354 @@ def _call(common, tail, target, q_rows, dt, sess, B, M, V, seed, round_, early):
         name = "sv_verify_sdcp"
         rc = lib().sv_verify_sdcp(*common, sess, B, M, V, *tail)
     return rc, name
+
+
+# ---------------------------------------------------------------------------
+# Per-session rules on logits and the state they keep (sv_adjust_logits,
+# sv_count_tokens, sv_grammar_masks, sv_grammar_advance).
+
+def make_penalties(B, repetition=1.0, frequency=0.0, presence=0.0, device="cuda"):
+    """Pack per-session penalties (scalars or length-B sequences) into the
+    [B] x 16-byte device array."""
+    import torch
+
+    s = np.zeros(B, dtype=PENALTIES_DTYPE)
+    s["repetition"], s["frequency"], s["presence"] = repetition, frequency, presence
+    for f in ("repetition", "frequency", "presence"):
+        if not np.isfinite(s[f]).all():
+            raise ValueError(f"{f} must be finite")
+    if not (s["repetition"] > 0).all():
+        raise ValueError("repetition must be positive")
+    return torch.from_numpy(s.view(np.uint8).reshape(B, 16).copy()).to(device)
+
+
+def make_history(n_slots, V, device="cuda"):
+    """An empty History of n_slots slots for a vocabulary of V tokens (V * 4 + V / 4
+    bytes a slot)."""
+    import torch
+
+    return History(torch.zeros((n_slots, V), dtype=torch.int32, device=device),
+                   torch.zeros((n_slots, 2, (V + 31) // 32), dtype=torch.int32, device=device))
+
+
+def make_bias(biases, V, device="cuda"):
+    """Bias from one {token: bias} mapping per session (empty or None: none)."""
+    import torch
+
+    offsets, ids, values = [0], [], []
+    for d in biases:
+        for t in sorted(d or ()):
+            if not 0 <= t < V:
+                raise ValueError(f"bias for token {t}, outside the vocabulary of {V}")
+            if not d[t] < float("inf"):
+                raise ValueError(f"bias of token {t} must be finite or -inf")
+            ids.append(t)
+            values.append(d[t])
+        offsets.append(len(ids))
+    return Bias(torch.tensor(offsets, dtype=torch.int32).to(device),
+                torch.tensor(ids, dtype=torch.int32).to(device),
+                torch.tensor(values, dtype=torch.float32).to(device))
+
+
+def make_masks(allowed, device="cuda"):
+    """[n, V] truth values (allowed tokens) as [n, W] int32 bit rows."""
+    import torch
+
+    a = np.asarray(allowed, dtype=bool)
+    if a.ndim != 2:
+        raise ValueError("allowed must be [n, V]")
+    full = np.zeros((a.shape[0], (a.shape[1] + 31) // 32 * 32), bool)
+    full[:, :a.shape[1]] = a
+    words = np.packbits(full, axis=1, bitorder="little").view("<i4")
+    return torch.from_numpy(words.copy()).to(device)
+
+
+def make_grammar(next_state, accept, device="cuda"):
+    """Grammar from next_state [n_states, 256] (a byte's next state, -1: refused) and
+    accept [n_states]: bytes that no state tells apart share a class."""
+    import torch
+
+    nxt = np.asarray(next_state)
+    if nxt.ndim != 2 or nxt.shape[1] != 256 or nxt.shape[0] < 1:
+        raise ValueError("next_state must be [n_states, 256]")
+    acc = np.asarray(accept).astype(bool).astype(np.uint8)
+    if acc.shape != (nxt.shape[0],):
+        raise ValueError("accept must be [n_states]")
+    if nxt.min() < -1 or nxt.max() >= nxt.shape[0]:
+        raise ValueError("next_state holds a state outside [-1, n_states)")
+    table, classes = np.unique(nxt, axis=1, return_inverse=True)
+    return Grammar(torch.from_numpy(np.ascontiguousarray(table, dtype=np.int32)).to(device),
+                   torch.from_numpy(classes.reshape(-1).astype(np.uint8)).to(device),
+                   torch.from_numpy(acc).to(device))
+
+
+def make_vocab(tokens, end=(), device="cuda"):
+    """Vocab from the tokens' byte strings (b"" for control tokens) and the ids of
+    the tokens that end a text (at most 8)."""
+    import torch
+
+    end = list(end)
+    if len(end) > 8 or any(not 0 <= t < len(tokens) for t in end):
+        raise ValueError("end must hold at most 8 ids of the vocabulary")
+    offsets = np.zeros(len(tokens) + 1, np.int64)
+    np.cumsum([len(t) for t in tokens], out=offsets[1:])
+    if offsets[-1] >= 1 << 31:
+        raise ValueError("the tokens' bytes exceed 2 GiB")
+    flat = np.frombuffer(b"".join(tokens), dtype=np.uint8)
+    return Vocab(torch.from_numpy(flat.copy()).to(device),
+                 torch.from_numpy(offsets.astype(np.int32)).to(device),
+                 torch.tensor(end, dtype=torch.int32).to(device))
+
+
+def _launch(dev, stream):
+    """(stream handle, context): the call's stream, and a context in which the
+    tensors' device is current and new tensors belong to that stream."""
+    import torch
+
+    here = torch.cuda.current_stream(dev)
+    if stream is None or stream.cuda_stream == here.cuda_stream:
+        stream, on = here, contextlib.nullcontext()
+    else:
+        on = torch.cuda.stream(stream)
+    if dev.index is not None and dev.index != torch.cuda.current_device():
+        both = contextlib.ExitStack()
+        both.enter_context(torch.cuda.device(dev))
+        both.enter_context(on)
+        on = both
+    return stream.cuda_stream, on
+
+
+def _device_of(t, name):
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a GPU tensor")
+    return t.device
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _history_struct(history, V, dev):
+    import torch
+
+    n = history.counts.shape[0]
+    _check(history.counts, "history.counts", torch.int32, (n, V), dev)
+    _check(history.seen, "history.seen", torch.int32, (n, 2, (V + 31) // 32), dev)
+    return _History(history.counts.data_ptr(), history.seen.data_ptr(), n)
+
+
+def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slots=None, bias=None,
+                  masks=None, mask_rows=None, out=None, status=None, stream=None):
+    """sv_adjust_logits: penalties for repeated tokens, biases and masks on a round's
+    logits, before verify().
+
+    logits [B, R, V] bf16/fp32, the last axis contiguous (a slice of a padded
+    vocabulary, or [R, B, V] transposed, will do); tokens [B, M] int32 the
+    round's drafted tokens: R = M + 1 target rows or R = M draft rows (None: R =
+    1, M = 0, a decoding step); m [B] int32 or None for M.  Each rule may be left
+    out: penalties [B, 16] uint8 (make_penalties) with history (make_history,
+    count_tokens) and slots [B] int32 (None: slot b); bias (make_bias); masks
+    [n, W] int32 bit rows (make_masks, grammar_masks) with mask_rows [B, R] int32
+    (-1: no mask).
+    out: None for a new contiguous tensor; a contiguous one like it; or logits
+    itself (in place, the rows then must not overlap).  Rows that a session does
+    not use are not written.  Returns dict(logits=out, status=[B] int32: 0, or
+    why a session failed, whose rows are then NaN).
+    """
+    import torch
+
+    dev = _device_of(logits, "logits")
+    if logits.dim() != 3 or 0 in logits.shape:
+        raise ValueError("logits must be a [B, R, V] tensor")
+    B, R, V = logits.shape
+    if logits.dtype == torch.bfloat16:
+        dt = BF16
+    elif logits.dtype == torch.float32:
+        dt = FP32
+    else:
+        raise TypeError("logits must be bfloat16 or float32")
+    sb, sr, sv_ = logits.stride()
+    if V > 1 and sv_ != 1:
+        raise ValueError("the logits of a row must be contiguous")
+    if tokens is None:
+        if R != 1:
+            raise ValueError("tokens may be left out only for one row a session")
+        M = 0
+        if m is not None:
+            raise ValueError("m needs tokens")
+    else:
+        M = R - 1 if tokens.dim() == 2 and tokens.shape[1] == R - 1 else R
+        _check(tokens, "tokens", torch.int32, (B, M), dev)
+        if m is not None:
+            _check(m, "m", torch.int32, (B,), dev)
+    if penalties is not None:
+        _check(penalties, "penalties", torch.uint8, (B, 16), dev)
+    hist = bs = mk = None
+    if history is not None:
+        hist = ctypes.byref(_history_struct(history, V, dev))
+        if slots is None and history.counts.shape[0] < B:
+            raise ValueError("history has fewer slots than sessions")
+    if slots is not None:
+        _check(slots, "slots", torch.int32, (B,), dev)
+    if bias is not None:
+        n = bias.ids.numel()
+        _check(bias.offsets, "bias.offsets", torch.int32, (B + 1,), dev)
+        _check(bias.ids, "bias.ids", torch.int32, (n,), dev)
+        _check(bias.values, "bias.values", torch.float32, (n,), dev)
+        bs = ctypes.byref(_Bias(bias.offsets.data_ptr(), bias.ids.data_ptr(),
+                                bias.values.data_ptr(), n))
+    if (masks is None) != (mask_rows is None):
+        raise ValueError("masks and mask_rows go together")
+    if masks is not None:
+        n = masks.shape[0]
+        _check(masks, "masks", torch.int32, (n, (V + 31) // 32), dev)
+        _check(mask_rows, "mask_rows", torch.int32, (B, R), dev)
+        if n < 1:
+            raise ValueError("masks must hold a row")
+        mk = ctypes.byref(_Masks(masks.data_ptr(), mask_rows.data_ptr(), n))
+    handle, on = _launch(dev, stream)
+    with on:
+        if out is None:
+            out = torch.empty((B, R, V), dtype=logits.dtype, device=dev)
+        elif out is not logits and out.data_ptr() == logits.data_ptr() and out.stride() == (sb, sr, sv_):
+            _check_like(out, logits)
+        elif out is not logits:
+            _check(out, "out", logits.dtype, (B, R, V), dev)
+            lo, hi = logits.data_ptr(), logits.data_ptr() + ((B - 1) * sb + (R - 1) * sr + V) * logits.element_size()
+            if out.data_ptr() < hi and lo < out.data_ptr() + out.numel() * out.element_size():
+                raise ValueError("out overlaps logits")
+        if out.data_ptr() == logits.data_ptr():
+            near, far = sorted(((sb, B), (sr, R)))
+            if (far[1] > 1 and far[0] < V) or (near[1] > 1 and near[0] < V) or \
+                    (far[1] > 1 and far[0] < (near[1] - 1) * near[0] + V):
+                raise ValueError("rows overlap: logits cannot be adjusted in place")
+        if status is None:
+            status = torch.empty(B, dtype=torch.int32, device=dev)
+        else:
+            _check(status, "status", torch.int32, (B,), dev)
+        rc = lib().sv_adjust_logits(logits.data_ptr(), sb, sr, dt, _ptr(tokens), _ptr(m),
+                                    _ptr(penalties), hist, _ptr(slots), bs, mk, B, M, R, V,
+                                    out.data_ptr(), status.data_ptr(), handle)
+    if rc != OK:
+        raise SvError(f"sv_adjust_logits failed: {strerror(rc)} ({rc})")
+    return {"logits": out, "status": status}
+
+
+def _check_like(out, logits):
+    if out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out must have the logits' shape and dtype")
+
+
+def count_tokens(history, tokens, slots=None, lens=None, offsets=None, prompt=False, clear=False,
+                 stream=None):
+    """sv_count_tokens: notes tokens in the history, in place.
+
+    tokens [B, L] int32, the first lens[b] (None: L) of each row; or, with offsets
+    [B + 1] int32, one line of tokens of which session b has offsets[b] ..
+    offsets[b + 1] - 1.  Tokens outside the vocabulary (the -1 of out_tokens) are
+    skipped.  slots [B] int32 (None: slot b; -1: skip).  prompt: prompt tokens
+    rather than output tokens; clear: empty the listed slots first.  After
+    commit(): count_tokens(history, out["out_tokens"], slots,
+    lens=out["emitted_len"])."""
+    import torch
+
+    dev = _device_of(tokens, "tokens")
+    V = history.counts.shape[-1]
+    hist = _history_struct(history, V, dev)
+    if offsets is not None:
+        if lens is not None:
+            raise ValueError("give lens or offsets, not both")
+        B, L = offsets.numel() - 1, tokens.numel()
+        _check(tokens, "tokens", torch.int32, (L,), dev)
+        _check(offsets, "offsets", torch.int32, (B + 1,), dev)
+    else:
+        if tokens.dim() != 2:
+            raise ValueError("tokens must be [B, L] (or one line, with offsets)")
+        B, L = tokens.shape
+        _check(tokens, "tokens", torch.int32, None, dev)
+        if lens is not None:
+            _check(lens, "lens", torch.int32, (B,), dev)
+    if slots is not None:
+        _check(slots, "slots", torch.int32, (B,), dev)
+    elif history.counts.shape[0] < B:
+        raise ValueError("history has fewer slots than sessions")
+    handle, on = _launch(dev, stream)
+    with on:
+        rc = lib().sv_count_tokens(ctypes.byref(hist), _ptr(slots), tokens.data_ptr(), _ptr(offsets),
+                                   _ptr(lens), B, L, V, 0 if prompt else 1, int(clear), handle)
+    if rc != OK:
+        raise SvError(f"sv_count_tokens failed: {strerror(rc)} ({rc})")
+
+
+def _grammar_structs(grammar, vocab, dev):
+    import torch
+
+    S, C = grammar.next.shape
+    V = vocab.offsets.numel() - 1
+    _check(grammar.next, "grammar.next", torch.int32, (S, C), dev)
+    _check(grammar.classes, "grammar.classes", torch.uint8, (256,), dev)
+    _check(grammar.accept, "grammar.accept", torch.uint8, (S,), dev)
+    _check(vocab.bytes, "vocab.bytes", torch.uint8, (vocab.bytes.numel(),), dev)
+    _check(vocab.offsets, "vocab.offsets", torch.int32, (V + 1,), dev)
+    _check(vocab.end, "vocab.end", torch.int32, (vocab.end.numel(),), dev)
+    g = _Grammar(grammar.next.data_ptr(), grammar.classes.data_ptr(), grammar.accept.data_ptr(), S, C)
+    v = _Vocab(vocab.bytes.data_ptr(), vocab.offsets.data_ptr(), vocab.end.data_ptr(),
+               vocab.bytes.numel(), vocab.end.numel(), V)
+    return ctypes.byref(g), ctypes.byref(v), V
+
+
+def grammar_masks(grammar, vocab, states, out=None, stream=None):
+    """sv_grammar_masks: the masks of automaton states, [n, W] int32 bit rows for
+    states [n] int32 (-1: every token allowed)."""
+    import torch
+
+    dev = _device_of(states, "states")
+    g, v, V = _grammar_structs(grammar, vocab, dev)
+    n = states.numel()
+    _check(states, "states", torch.int32, (n,), dev)
+    handle, on = _launch(dev, stream)
+    with on:
+        if out is None:
+            out = torch.empty((n, (V + 31) // 32), dtype=torch.int32, device=dev)
+        else:
+            _check(out, "out", torch.int32, (n, (V + 31) // 32), dev)
+        rc = lib().sv_grammar_masks(g, v, states.data_ptr(), n, out.data_ptr(), handle)
+    if rc != OK:
+        raise SvError(f"sv_grammar_masks failed: {strerror(rc)} ({rc})")
+    return out
+
+
+def grammar_advance(grammar, vocab, states, tokens, lens=None, out=None, stream=None):
+    """sv_grammar_advance: automaton states along tokens [B, L] int32 (the first
+    lens[b], None: L) from states [B] int32 (-1: no grammar).  Returns
+    dict(states=[B, L + 1] int32, the states after 0, 1, .. tokens; last=[B] int32,
+    the state after all of them).  states, passed as mask_rows with the masks of
+    all states, are the masks of a round's rows."""
+    import torch
+
+    dev = _device_of(tokens, "tokens")
+    g, v, _ = _grammar_structs(grammar, vocab, dev)
+    if tokens.dim() != 2:
+        raise ValueError("tokens must be [B, L]")
+    B, L = tokens.shape
+    _check(tokens, "tokens", torch.int32, None, dev)
+    _check(states, "states", torch.int32, (B,), dev)
+    if lens is not None:
+        _check(lens, "lens", torch.int32, (B,), dev)
+    handle, on = _launch(dev, stream)
+    with on:
+        if out is None:
+            out = {"states": torch.empty((B, L + 1), dtype=torch.int32, device=dev),
+                   "last": torch.empty(B, dtype=torch.int32, device=dev)}
+        else:
+            _check(out["states"], "out['states']", torch.int32, (B, L + 1), dev)
+            _check(out["last"], "out['last']", torch.int32, (B,), dev)
+        rc = lib().sv_grammar_advance(g, v, states.data_ptr(), tokens.data_ptr(), _ptr(lens), B, L,
+                                      out["states"].data_ptr(), out["last"].data_ptr(), handle)
+    if rc != OK:
+        raise SvError(f"sv_grammar_advance failed: {strerror(rc)} ({rc})")
+    return out

@@ -328,6 +328,7 @@ extern "C" const char* sv_status_str(int status) {
     case SV_S_Q_UNAVAILABLE: return "sdcp-q-unavailable: rule 2 without draft logits";
     case SV_S_BAD_PROFILE: return "bad profile: unknown rule, top_p_milli > 1000 or reserved != 0";
     case SV_S_BAD_LOGITS: return "bad logits: NaN or +inf, or no finite logit, in a row read";
+    case SV_S_BAD_CONTROL: return "bad control: penalties, history slot, bias offsets or mask row out of range";
     default: return "unknown status";
   }
 }
