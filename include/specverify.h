@@ -396,7 +396,7 @@ int sv_verify_noalloc(const void *target_logits, const void *draft_logits, int32
 
 /* Per-session penalties for repeated tokens, 16 bytes; a DEVICE array [B]. */
 typedef struct sv_penalties {
-  float repetition;  /* finite and > 0; 1 = off */
+  float repetition;  /* 2^-64 .. 2^64; 1 = off */
   float frequency;   /* finite; 0 = off */
   float presence;    /* finite; 0 = off */
   uint32_t reserved; /* must be 0 */

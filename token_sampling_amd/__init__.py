@@ -578,8 +578,8 @@ def make_penalties(B, repetition=1.0, frequency=0.0, presence=0.0, device="cuda"
     for f in ("repetition", "frequency", "presence"):
         if not np.isfinite(s[f]).all():
             raise ValueError(f"{f} must be finite")
-    if not (s["repetition"] > 0).all():
-        raise ValueError("repetition must be positive")
+    if not ((s["repetition"] >= 2.0**-64) & (s["repetition"] <= 2.0**64)).all():
+        raise ValueError("repetition must be within 2^-64 .. 2^64")
     return torch.from_numpy(s.view(np.uint8).reshape(B, 16).copy()).to(device)
 
 
