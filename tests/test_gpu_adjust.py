@@ -257,6 +257,27 @@ def test_bias_offsets_out_of_range():
     both_ways(case)
 
 
+@pytest.mark.parametrize("V", [301, 1022, 4093])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_bits_past_the_vocabulary(V, dtype):
+    """Bits at and past V of the history and of masks say nothing."""
+    case = Case(45, 3, 2, 3, V, dtype)
+    past = np.zeros((V + 31) // 32 * 32, bool)
+    past[V:] = True
+    junk = ref.pack(past[None])[0]
+    case.seen |= junk
+    case.masks |= junk
+    B, R = 3, 3
+    x = torch.full((B, R, V + 40), 9.0, dtype=case.logits.dtype, device="cuda")
+    view = x[:, :, :V]
+    view.copy_(case.logits)
+    case.run(logits=view, out=view)
+    torch.cuda.synchronize()
+    case.check(view, case.logits)
+    assert (x[:, :, V:] == 9.0).all()
+    both_ways(case)
+
+
 def test_binding_refusals():
     case = Case(44, 2, 2, 3, 64, "fp32")
     x = case.logits.cuda()

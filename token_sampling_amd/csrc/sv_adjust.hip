@@ -14,9 +14,17 @@
 namespace sv {
 namespace {
 
-constexpr int kWaves = 4;  // per workgroup; each works by itself
+#ifndef SV_ADJUST_WAVES
+#define SV_ADJUST_WAVES 4
+#endif
+constexpr int kWaves = SV_ADJUST_WAVES;  // per workgroup; each works by itself
 constexpr int64_t kWantedWaves = 8192;   // two for each place of a wave in the card's SIMDs
-constexpr int64_t kMaxGroups = 1 << 22;  // keeps the launch's work-items within 32 bits
+constexpr int kGridY = 32768;  // sessions of a launch
+constexpr int kScan = 4;       // 64s of biases that a wave looks through without a search
+#ifndef SV_ADJUST_BATCH
+#define SV_ADJUST_BATCH 4
+#endif
+constexpr int kBatch = SV_ADJUST_BATCH;  // rows in flight together
 #ifndef SV_ADJUST_GROUPS
 #define SV_ADJUST_GROUPS 2
 #endif
@@ -40,15 +48,33 @@ struct AdjustArgs {
   const uint32_t* mask_bits;
   const int32_t* mask_rows;
   int32_t n_masks;
-  int32_t B, M, R, V, W, n_tiles, n_chunks, chunk;
+  int32_t B, M, R, V, W;
+  int32_t chunk;  // rows of a unit of work
+  int32_t b0;     // the launch's first session
   int32_t* status;
 };
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 struct __attribute__((packed, aligned(2))) Vec16b {
   u32x4 v;
 };
+
+__device__ inline u32x4 load16(const void* p) {
+#if SV_NT & 1
+  typedef unsigned int uu __attribute__((ext_vector_type(4), aligned(2)));
+  return __builtin_nontemporal_load((const uu*)p);
+#else
+  return ((const Vec16b*)p)->v;
+#endif
+}
+__device__ inline void store16(void* p, u32x4 v) {
+#if SV_NT & 2
+  typedef unsigned int uu __attribute__((ext_vector_type(4), aligned(2)));
+  __builtin_nontemporal_store((uu)v, (uu*)p);
+#else
+  ((Vec16b*)p)->v = v;
+#endif
+}
 
 // A lane's share of a row: one 16-byte vector per group, 8 bf16 or 4 binary32
 // logits, 64 lanes side by side.
@@ -71,53 +97,48 @@ struct Session {
   int32_t mask_row;   // lane r: the mask of row r
   int32_t mask_row64; // row 64's
   int bias_lo, bias_hi;
-  sv_penalties pen;
+  float repetition, frequency, presence;
 };
 
+// All of a session's controls come with three loads that do not wait for each
+// other: lane by lane the single values, the drafted tokens, the rows' masks.
 __device__ inline Session session_of(const AdjustArgs& a, int b) {
   const int lane = __lane_id();
+  const int32_t* p = nullptr;
+  if (lane == 0 && a.m) p = a.m + b;
+  if (lane == 1 && a.slots) p = a.slots + b;
+  if (lane >= 2 && lane < 6 && a.pen) p = (const int32_t*)(a.pen + b) + (lane - 2);
+  if (lane >= 6 && lane < 8 && a.bias_off) p = a.bias_off + b + (lane - 6);
+  if (lane == 8 && a.mask_rows && a.R > kWave) p = a.mask_rows + (size_t)b * a.R + kWave;
+  int32_t value = 0, token = -1, mask_row = -1;
+  if (p) value = *p;
+  if (a.pen && lane < a.M) token = a.tokens[(size_t)b * a.M + lane];
+  if (a.mask_rows && lane < a.R) mask_row = a.mask_rows[(size_t)b * a.R + lane];
+
   Session s;
-  s.status = 0;
-  s.slot = -1;
-  s.token = -1;
-  s.mask_row = s.mask_row64 = -1;
-  s.bias_lo = s.bias_hi = 0;
-  s.pen = {1.f, 0.f, 0.f, 0};
-  s.m = a.m ? a.m[b] : a.M;
-  if (s.m < 0 || s.m > a.M) {
-    s.status = SV_S_LIMIT;
-    return s;
-  }
+  s.m = a.m ? lane_read(value, 0) : a.M;
+  s.slot = a.counts == nullptr ? -1 : a.slots ? lane_read(value, 1) : b;
+  s.repetition = a.pen ? __builtin_bit_cast(float, lane_read(value, 2)) : 1.f;
+  s.frequency = __builtin_bit_cast(float, lane_read(value, 3));
+  s.presence = __builtin_bit_cast(float, lane_read(value, 4));
+  s.bias_lo = lane_read(value, 6);
+  s.bias_hi = lane_read(value, 7);
   const int rows = s.m + (a.R - a.M);
-  bool bad = false, bad_token = false;
-  if (a.pen) {
-    if (lane < s.m) {
-      s.token = a.tokens[(size_t)b * a.M + lane];
-      bad_token = s.token < 0 || s.token >= a.V;
-    }
-    const sv_penalties p = a.pen[b];
-    // within these bounds the reciprocal is a normal number
-    bad |= !(p.repetition >= 0x1p-64f && p.repetition <= 0x1p64f) || !isfinite(p.frequency) ||
-           !isfinite(p.presence) || p.reserved != 0;
-    if (a.counts) {
-      s.slot = a.slots ? a.slots[b] : b;
-      bad |= s.slot < -1 || s.slot >= a.n_slots;
-    }
-    s.pen = p;
-  }
-  if (a.bias_off) {
-    s.bias_lo = a.bias_off[b];
-    s.bias_hi = a.bias_off[b + 1];
-    bad |= s.bias_lo < 0 || s.bias_hi < s.bias_lo || s.bias_hi > a.n_bias;
-  }
-  if (a.mask_rows) {
-    const int32_t* k = a.mask_rows + (size_t)b * a.R;
-    if (lane < rows) s.mask_row = k[lane];
-    if (rows > kWave) s.mask_row64 = k[kWave];
-    bad |= s.mask_row < -1 || s.mask_row >= a.n_masks || s.mask_row64 < -1 ||
-           s.mask_row64 >= a.n_masks;
-  }
-  s.status = __any(bad) ? SV_S_BAD_CONTROL : __any(bad_token) ? SV_S_BAD_PROPOSAL : 0;
+  s.mask_row = lane < rows ? mask_row : -1;
+  s.mask_row64 = a.mask_rows && rows > kWave ? lane_read(value, 8) : -1;
+  s.token = lane < s.m ? token : -1;
+  // a reciprocal of a repetition within these bounds is a normal number
+  const bool bad =
+      !(s.repetition >= 0x1p-64f && s.repetition <= 0x1p64f) || !isfinite(s.frequency) ||
+      !isfinite(s.presence) || (a.pen && lane_read(value, 5) != 0) || s.slot < -1 ||
+      (a.counts != nullptr && s.slot >= a.n_slots) || s.bias_lo < 0 || s.bias_hi < s.bias_lo ||
+      s.bias_hi > a.n_bias || s.mask_row < -1 || (a.mask_rows && s.mask_row >= a.n_masks) ||
+      s.mask_row64 < -1 || (a.mask_rows && s.mask_row64 >= a.n_masks);
+  const bool bad_token = a.pen && lane < s.m && (token < 0 || token >= a.V);
+  s.status = s.m < 0 || s.m > a.M ? SV_S_LIMIT
+             : __any(bad)         ? SV_S_BAD_CONTROL
+             : __any(bad_token)   ? SV_S_BAD_PROPOSAL
+                                  : 0;
   return s;
 }
 
@@ -139,15 +160,6 @@ __device__ inline int lower_bound(const int32_t* ids, int lo, int hi, int v) {
   return lo;
 }
 
-__device__ inline float widen(const u32x4& x, int i, __bf16) {
-  const uint32_t w = x[i / 2];
-  return __builtin_bit_cast(float, i % 2 ? w & 0xFFFF0000u : w << 16);
-}
-__device__ inline float widen(const u32x4& x, int i, float) {
-  const uint32_t w = x[i];
-  return __builtin_bit_cast(float, w);
-}
-
 // All ones where bit i of bits is set, else zeros.
 __device__ inline uint32_t spread(uint32_t bits, int i) {
   return (uint32_t)__builtin_amdgcn_sbfe((int)bits, i, 1);
@@ -159,266 +171,338 @@ __device__ inline uint32_t select_word(uint32_t bits, int d, __bf16) {
 }
 __device__ inline uint32_t select_word(uint32_t bits, int d, float) { return spread(bits, d); }
 
-__device__ inline uint32_t round_word(const float* z, int d, __bf16) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 h = {(__bf16)z[2 * d], (__bf16)z[2 * d + 1]};
-  return __builtin_bit_cast(uint32_t, h);
-}
-__device__ inline uint32_t round_word(const float* z, int d, float) {
-  return __builtin_bit_cast(uint32_t, z[d]);
-}
+// A logit's bits, zero-extended, and its value: the wait for the load comes with
+// the second.
+__device__ inline uint32_t load_bits(const __bf16* p) { return *(const uint16_t*)p; }
+__device__ inline uint32_t load_bits(const float* p) { return *(const uint32_t*)p; }
+__device__ inline float from_bits(uint32_t x, __bf16) { return __builtin_bit_cast(float, x << 16); }
+__device__ inline float from_bits(uint32_t x, float) { return __builtin_bit_cast(float, x); }
 
 template <typename T>
 constexpr uint32_t kMinusInf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
 
+// A touched token of a tile, 16 bits: its place in the tile and
+constexpr uint32_t kPlace = 0x0FFF;
+constexpr uint32_t kRep = 0x1000;   // seen: the repetition penalty applies
+constexpr uint32_t kHad = 0x2000;   // output before: its presence is counted
+constexpr uint32_t kOn = 0x4000;    // a rule changes it (not yet, for a drafted token ahead)
+constexpr uint32_t kBias = 0x8000;  // it has a bias
+
 // One wave works on one unit: kTile neighbouring tokens of one session, row
-// after row.  What the rows share is set up once: an additive term for each
-// token that the history, a bias or a drafted token touches (in LDS, the
-// wave's own), and three bits a token in registers: rep (seen, the repetition
-// penalty applies), had (output, so no presence any more) and hot (the token
-// changes).  Row r then adds what x_r changes, which only the tiles holding
-// x_r do, and streams: a vector without hot tokens and with a full mask is a
-// copy (in place: not touched), one with an empty mask is not read.
+// after row.  What the rows share is set up once, in the wave's own LDS: the
+// list of the tokens that the history, a bias or a drafted token touches, and
+// an additive term for each.  Then the rows stream in 16-byte vectors, a few
+// thousand tokens a row out of 1e5 passing through LDS on the way, where one
+// lane a listed token changes them: with every lane working out its own
+// vector's changes instead, a wave took 200 vector instructions a row and tile
+// and the kernel was bound by them in place.  Vectors with an empty mask are
+// not read; in place, rows without a mask move their listed tokens alone.
 template <typename T, int G, bool kInPlace>
 __global__ __launch_bounds__(kWaves* kWave) void k_adjust(AdjustArgs a) {
   using L = Lanes<T>;
   constexpr int E = L::kE, kTile = G * L::kGroup;
-  constexpr uint32_t kAll = (1u << E) - 1;
-  static_assert(G * E <= 32, "a lane's tokens fit one word");
-  __shared__ __attribute__((aligned(16))) float lds_term[kWaves][kTile];
+  constexpr uint32_t kAll = (1u << E) - 1;  // one vector's tokens
+  constexpr uint32_t kFull = G * E == 32 ? ~0u : (1u << (G * E)) - 1;
+  static_assert(G * E <= 32 && kTile <= (int)kPlace + 1, "a lane's tokens fit one word");
+  __shared__ __attribute__((aligned(16))) T lds_raw[kWaves][kTile];
+  __shared__ float lds_term[kWaves][kTile];
+  __shared__ uint16_t lds_list[kWaves][kTile];
   __shared__ uint32_t lds_bits[kWaves][kTile / 32];
   const int lane = __lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  T* raw = lds_raw[wave];
   float* term = lds_term[wave];
+  uint16_t* list = lds_list[wave];
   uint32_t* bits = lds_bits[wave];
-  const int64_t units = (int64_t)a.B * a.n_tiles * a.n_chunks;
-  const T nil = T(0);
+  const int tile = blockIdx.x * kWaves + wave;
+  const int v0 = tile * kTile;
+  if (v0 >= a.V) return;
+  const int first = lane * E;   // a lane's vectors start at first + g * kGroup
+  const int left = a.V - v0;    // tokens from the tile's start to the row's end
+  const int chunk = blockIdx.z;
+  uint32_t within = 0;  // a lane's tokens that the row has
+#pragma unroll
+  for (int g = 0; g < G; ++g) {
+    const int n = left - g * L::kGroup - first;
+    within |= (n >= E ? kAll : n > 0 ? (1u << n) - 1 : 0u) << (g * E);
+  }
 
-  for (int64_t u0 = (int64_t)blockIdx.x * kWaves; u0 < units; u0 += (int64_t)gridDim.x * kWaves) {
-    const int64_t u = u0 + wave;
-    if (u >= units) break;
-    const int tile = (int)(u % a.n_tiles);
-    const int64_t bc = u / a.n_tiles;
-    const int b = (int)(bc / a.n_chunks), chunk = (int)(bc % a.n_chunks);
-    const int v0 = tile * kTile;
-    const Session s = session_of(a, b);
-    if (a.status && tile == 0 && chunk == 0 && lane == 0) a.status[b] = s.status;
-    const int rows = s.status == 0 ? s.m + (a.R - a.M) : a.R;
-    const int r0 = chunk * a.chunk, r1 = r0 + a.chunk < rows ? r0 + a.chunk : rows;
-    if (r0 >= r1) continue;
-    const T* in = (const T*)a.logits + b * a.in_session + v0;
-    T* out = (T*)a.out + b * a.out_session + v0;
+  const int b = a.b0 + blockIdx.y;
+  const Session s = session_of(a, b);
+  if (a.status && tile == 0 && chunk == 0 && lane == 0) a.status[b] = s.status;
+  const int rows = s.status == 0 ? s.m + (a.R - a.M) : a.R;
+  const int r0 = chunk * a.chunk, r1 = r0 + a.chunk < rows ? r0 + a.chunk : rows;
+  if (r0 >= r1) return;
+  const T* in = (const T*)a.logits + b * a.in_session + v0;
+  T* out = (T*)a.out + b * a.out_session + v0;
+  if (s.status != 0) {
+    for (int r = r0; r < r1; ++r)
+      for (int i = lane; i < kTile && i < left; i += kWave)
+        out[r * a.out_row + i] = (T)__builtin_nanf("");
+    return;
+  }
 
-    // a lane's vectors: tokens v0 + first + g * kGroup ...
-    const int first = lane * E;
-    const int left = a.V - v0;  // tokens from the tile's start to the row's end
-    if (s.status != 0) {
-      for (int r = r0; r < r1; ++r)
-        for (int i = lane; i < kTile && i < left; i += kWave)
-          out[r * a.out_row + i] = (T)__builtin_nanf("");
+  // A lane's bits of a bit row over the vocabulary: the bytes that hold them,
+  // and those packed vector by vector, none past the row's end.
+  struct Bytes {
+    uint32_t of[G];
+  };
+  auto bytes_of = [&](const uint32_t* words) {
+    Bytes y;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int v = v0 + g * L::kGroup + first;
+      y.of[g] = ((const uint8_t*)words)[(v < a.V ? v : a.V - 1) / 8];
+    }
+    return y;
+  };
+  auto packed = [&](const Bytes& y) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) w |= ((y.of[g] >> (first % 8)) & kAll) << (g * E);
+    return w & within;
+  };
+  auto mask_row = [&](int r) {
+    if (a.mask_rows == nullptr || r >= r1) return -1;
+    return r < kWave ? lane_read(s.mask_row, r) : s.mask_row64;
+  };
+  auto mask_of = [&](int k) {
+    return k < 0 ? kFull : packed(bytes_of(a.mask_bits + (size_t)k * a.W));
+  };
+  auto load = [&](int r, uint32_t mk, uint32_t needed, u32x4 (&x)[G]) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int i = g * L::kGroup + first;
+      x[g] = u32x4{0, 0, 0, 0};
+      if (((mk >> (g * E)) & kAll) != 0 && ((needed >> (g * E)) & kAll) != 0 && i < left) {
+        const T* p = in + r * a.in_row + i;
+        if (i + E <= left) {
+          x[g] = load16(p);
+        } else {
+          T t[E];
+#pragma unroll
+          for (int k = 0; k < E; ++k) t[k] = i + k < left ? p[k] : T(0);
+          __builtin_memcpy(&x[g], t, 16);
+        }
+      }
+    }
+  };
+
+  // ---- what the rows share; loads first
+  Bytes prompt = {}, output = {}, mask = {};
+  if (s.slot >= 0) {
+    const uint32_t* seen = a.seen + (size_t)s.slot * 2 * a.W;
+    prompt = bytes_of(seen);
+    output = bytes_of(seen + a.W);
+  }
+  const int mask0 = mask_row(r0);
+  if (mask0 >= 0) mask = bytes_of(a.mask_bits + (size_t)mask0 * a.W);
+  int bias_lo = s.bias_lo, bias_hi = s.bias_hi;
+  if (bias_hi - bias_lo > kScan * kWave) {
+    bias_lo = lower_bound(a.bias_id, bias_lo, bias_hi, v0);
+    bias_hi = lower_bound(a.bias_id, bias_lo, bias_hi, v0 + kTile);
+  }
+  int32_t id[kScan];
+  float bias[kScan];
+#pragma unroll
+  for (int c = 0; c < kScan; ++c) {
+    const int e = bias_lo + c * kWave + lane;
+    id[c] = -1;
+    bias[c] = 0.f;
+    if (e < bias_hi) {
+      id[c] = a.bias_id[e];
+      bias[c] = a.bias_val[e];
+    }
+  }
+  u32x4 x[G];
+  uint32_t mk = mask0 < 0 ? kFull : packed(mask);
+  if constexpr (!kInPlace) load(r0, mk, kFull, x);
+
+  const uint32_t had = packed(output), rep = packed(prompt) | had;
+  // drafted tokens of this tile that rows before r1 meet
+  const uint64_t mine = __ballot(s.token >= v0 && s.token - v0 < kTile && lane < r1 - 1);
+  uint32_t biased = 0, any = rep;
+  auto here = [&](int v) { return v >= v0 && v < a.V && v - v0 < kTile; };
+  bool biases = bias_hi - bias_lo > kScan * kWave;
+#pragma unroll
+  for (int c = 0; c < kScan; ++c) biases |= here(id[c]);
+  if (mine != 0 || __any(biases)) {
+    if (lane < kTile / 32) bits[lane] = 0;
+    wave_sync();
+    auto note = [&](int v, float t) {
+      if (!here(v)) return;
+      atomicOr(bits + (v - v0) / 32, 1u << ((v - v0) % 32));
+      term[v - v0] = t;
+    };
+#pragma unroll
+    for (int c = 0; c < kScan; ++c) note(id[c], bias[c]);
+    for (int e = bias_lo + kScan * kWave + lane; e < bias_hi; e += kWave)
+      note(a.bias_id[e], a.bias_val[e]);
+    wave_sync();
+    auto noted = [&] {
+      uint32_t w = 0;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int i = g * L::kGroup + first;
+        w |= ((bits[i / 32] >> (i % 32)) & kAll) << (g * E);
+      }
+      return w;
+    };
+    biased = noted();
+    wave_sync();
+    if ((mine >> lane) & 1) atomicOr(bits + (s.token - v0) / 32, 1u << ((s.token - v0) % 32));
+    wave_sync();
+    any |= noted();
+  }
+  const int count = __popc(any);
+  const int upto = wave_incl_scan(count);
+  const int listed = lane_read(upto, kWave - 1);
+  if (listed > 0) {
+    int at = upto - count;
+    for (uint32_t w = any; w != 0; w &= w - 1) {
+      const int k = __builtin_ctz(w);
+      const uint32_t bit = 1u << k;
+      uint32_t e = (k / E) * L::kGroup + first + k % E;
+      if (rep & bit) e |= kRep | kOn;
+      if (had & bit) e |= kHad;
+      if (biased & bit) e |= kBias | kOn;
+      list[at++] = (uint16_t)e;
+    }
+    wave_sync();
+    for (int j = lane; j < listed; j += kWave) {
+      const uint32_t e = list[j];
+      const int i = e & kPlace;
+      float t = e & kBias ? term[i] : 0.f;
+      if (e & kHad) {
+        const int c = a.counts[(size_t)s.slot * a.V + v0 + i];
+        if (c > 0) t -= s.frequency * (float)c + s.presence;
+      }
+      term[i] = t;
+    }
+    wave_sync();
+  }
+
+  // ---- the rows
+  const uint64_t masked = __ballot(s.mask_row >= 0);
+  const float up = s.repetition, down = 1.f / s.repetition;
+  auto changed = [&](float z, uint32_t e, float t) {
+    const float f = z > 0.f ? down : up;
+    return (e & kRep ? z * f : z) + t;
+  };
+  auto meet = [&](int d) {  // drafted token d counts from here on
+    const int place = lane_read(s.token, d) - v0;
+    for (int j = lane; j < listed; j += kWave) {
+      const uint32_t e = list[j];
+      if ((int)(e & kPlace) == place) {
+        term[place] -= e & kHad ? s.frequency : s.frequency + s.presence;
+        list[j] = (uint16_t)(e | kRep | kHad | kOn);
+      }
+    }
+    wave_sync();
+  };
+  for (int d = 0; d < r0; ++d)
+    if ((mine >> d) & 1) meet(d);
+
+  for (int r = r0; r < r1;) {
+    if (r > r0 && ((mine >> (r - 1)) & 1)) meet(r - 1);
+    if (kInPlace && mask_row(r) < 0) {
+      // rows alike: up to the next that meets a token of this tile or has a mask
+      int n = r1 - r;
+      const uint64_t met = r < kWave ? mine >> r : 0, held = r < kWave ? masked >> r : 0;
+      if (met != 0) n = min(n, __builtin_ctzll(met) + 1);
+      if (held != 0) n = min(n, __builtin_ctzll(held));
+      if (s.mask_row64 >= 0) n = min(n, kWave - r);
+      // lanes: 2^p listed tokens by 64 / 2^p rows
+      const int p = listed > 32 ? 6 : listed > 1 ? 32 - __builtin_clz(listed - 1) : 0;
+      const int step = kWave >> p;
+      for (int j = lane & ((1 << p) - 1); j < listed; j += kWave) {
+        const uint32_t e = list[j];
+        const int i = e & kPlace;
+        const float t = term[i];
+        if (!(e & kOn)) continue;
+        for (int q0 = lane >> p; q0 < n; q0 += kBatch * step) {
+          uint32_t z[kBatch];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k)
+            z[k] = load_bits(in + (r + min(q0 + k * step, n - 1)) * a.in_row + i);
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k)
+            if (q0 + k * step < n)
+              out[(r + q0 + k * step) * a.out_row + i] = (T)changed(from_bits(z[k], T(0)), e, t);
+        }
+      }
+      r += n;
       continue;
     }
-
-    // ---- what the rows share
-    uint32_t rep = 0, had = 0, hot = 0;
-    // drafted tokens of this tile that rows before r1 meet
-    const uint64_t mine =
-        __ballot(s.token >= v0 && s.token - v0 < kTile && lane < r1 - 1);
-    const uint32_t* seen = a.seen;
-    if (s.slot >= 0) {
-      seen += (size_t)s.slot * 2 * a.W;
+    const uint32_t next = mask_of(mask_row(r + 1));
+    // in place: the vectors that change (any has a bit for each listed token)
+    if constexpr (kInPlace) {
+      mk = mask_of(mask_row(r));
+      load(r, mk, any | (mk ^ kFull), x);
+    }
+    u32x4 y[G];
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int v = v0 + g * L::kGroup + first;
-        if (v < a.V) {
-          const uint32_t p = ((const uint8_t*)seen)[v / 8] >> (v % 8);
-          const uint32_t o = ((const uint8_t*)(seen + a.W))[v / 8] >> (v % 8);
-          rep |= ((p | o) & kAll) << (g * E);
-          had |= (o & kAll) << (g * E);
+    for (int g = 0; g < G; ++g) y[g] = x[g];
+    if constexpr (!kInPlace) {
+      if (r + 1 < r1) load(r + 1, next, kFull, x);
+    }
+    if (listed > 0) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if ((any >> (g * E)) & kAll) *(u32x4*)(raw + g * L::kGroup + first) = y[g];
+      wave_sync();
+      for (int j = lane; j < listed; j += kWave) {
+        const uint32_t e = list[j];
+        const int i = e & kPlace;
+        if (e & kOn) raw[i] = (T)changed((float)raw[i], e, term[i]);
+      }
+      wave_sync();
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if ((any >> (g * E)) & kAll) y[g] = *(const u32x4*)(raw + g * L::kGroup + first);
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int i = g * L::kGroup + first;
+      const uint32_t ok = (mk >> (g * E)) & kAll;
+      if (i >= left || (kInPlace && ((any >> (g * E)) & kAll) == 0 && ok == kAll)) continue;
+      if (ok != kAll) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const uint32_t sel = select_word(ok, d, T(0)), w = y[g][d];
+          y[g][d] = (w & sel) | (kMinusInf<T> & ~sel);
         }
       }
-    }
-    int bias_lo = 0, bias_hi = 0;
-    if (s.bias_lo < s.bias_hi) {
-      bias_lo = lower_bound(a.bias_id, s.bias_lo, s.bias_hi, v0);
-      bias_hi = lower_bound(a.bias_id, bias_lo, s.bias_hi, v0 + kTile);
-    }
-    hot = rep;
-    uint32_t groups = hot;  // tokens whose vectors need terms
-    if (mine != 0 || bias_lo < bias_hi) {
-      if (lane < kTile / 32) bits[lane] = 0;
-      wave_sync();
-      for (int e = bias_lo + lane; e < bias_hi; e += kWave) {
-        const int i = a.bias_id[e] - v0;
-        if (i >= 0 && i < kTile) atomicOr(bits + i / 32, 1u << (i % 32));
-      }
-      wave_sync();
-      uint32_t biased = 0;
+      T* p = out + r * a.out_row + i;
+      if (i + E <= left) {
+        store16(p, y[g]);
+      } else {
+        T t[E];
+        __builtin_memcpy(t, &y[g], 16);
 #pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int i = g * L::kGroup + first;
-        biased |= ((bits[i / 32] >> (i % 32)) & kAll) << (g * E);
-      }
-      hot |= biased;
-      wave_sync();
-      if ((mine >> lane) & 1) atomicOr(bits + (s.token - v0) / 32, 1u << ((s.token - v0) % 32));
-      wave_sync();
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int i = g * L::kGroup + first;
-        groups |= ((bits[i / 32] >> (i % 32)) & kAll) << (g * E);
-      }
-      groups |= hot;
-    }
-    if (__any(groups != 0)) {
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        if (((groups >> (g * E)) & kAll) == 0) continue;
-        const int i = g * L::kGroup + first, v = v0 + i;
-        const uint32_t o = (had >> (g * E)) & kAll;
-        float t[E];
-#pragma unroll
-        for (int k = 0; k < E; ++k) t[k] = 0.f;
-        if (o != 0) {
-          int32_t c[E];
-          const int32_t* row = a.counts + (size_t)s.slot * a.V + v;
-          if (v + E <= a.V) {
-            __builtin_memcpy(c, row, sizeof(c));
-          } else {
-#pragma unroll
-            for (int k = 0; k < E; ++k) c[k] = v + k < a.V ? row[k] : 0;
-          }
-#pragma unroll
-          for (int k = 0; k < E; ++k)
-            if ((o >> k) & 1 && c[k] > 0) t[k] = -(s.pen.frequency * (float)c[k] + s.pen.presence);
-        }
-#pragma unroll
-        for (int k = 0; k < E; k += 4) *(f32x4*)(term + i + k) = f32x4{t[k], t[k + 1], t[k + 2], t[k + 3]};
-      }
-      wave_sync();
-      for (int e = bias_lo + lane; e < bias_hi; e += kWave) {
-        const int i = a.bias_id[e] - v0;
-        if (i >= 0 && i < kTile) term[i] += a.bias_val[e];
-      }
-      wave_sync();
-    }
-
-    // ---- the rows
-    const float up = s.pen.repetition, down = 1.f / s.pen.repetition;
-    auto meet = [&](int j) {  // drafted token j counts from here on
-      const int i = lane_read(s.token, j) - v0;
-      const int g = i / L::kGroup;
-      if (lane == (i % L::kGroup) / E) {
-        const uint32_t bit = 1u << (g * E + i % E);
-        term[i] -= had & bit ? s.pen.frequency : s.pen.frequency + s.pen.presence;
-        had |= bit;
-        rep |= bit;
-        hot |= bit;
-      }
-      wave_sync();
-    };
-    for (int j = 0; j < r0; ++j)
-      if ((mine >> j) & 1) meet(j);
-
-    auto mask_of = [&](int r, uint32_t (&mk)[G]) {
-#pragma unroll
-      for (int g = 0; g < G; ++g) mk[g] = kAll;
-      if (a.mask_rows == nullptr || r >= r1) return;
-      const int k = r < kWave ? lane_read(s.mask_row, r) : s.mask_row64;
-      if (k < 0) return;
-      const uint8_t* row = (const uint8_t*)(a.mask_bits + (size_t)k * a.W);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int v = v0 + g * L::kGroup + first;
-        if (v < a.V) mk[g] = ((uint32_t)row[v / 8] >> (v % 8)) & kAll;
-      }
-    };
-    uint32_t mk[G];
-    mask_of(r0, mk);
-    for (int r = r0; r < r1; ++r) {
-      if (r > r0 && ((mine >> (r - 1)) & 1)) meet(r - 1);
-      u32x4 x[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int i = g * L::kGroup + first;
-        const uint32_t h = (hot >> (g * E)) & kAll;
-        x[g] = u32x4{0, 0, 0, 0};
-        if (mk[g] != 0 && i < left && (!kInPlace || h != 0 || mk[g] != kAll)) {
-          const T* p = in + r * a.in_row + i;
-          if (i + E <= left) {
-            x[g] = ((const Vec16b*)p)->v;
-          } else {
-            T t[E];
-#pragma unroll
-            for (int k = 0; k < E; ++k) t[k] = i + k < left ? p[k] : nil;
-            __builtin_memcpy(&x[g], t, 16);
-          }
-        }
-      }
-      uint32_t next[G];
-      mask_of(r + 1, next);
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int i = g * L::kGroup + first;
-        const uint32_t h = (hot >> (g * E)) & kAll;
-        if (i < left && (!kInPlace || h != 0 || mk[g] != kAll)) {
-          if (h != 0) {
-            float z[E];
-#pragma unroll
-            for (int k = 0; k < E; k += 4) {
-              const f32x4 t = *(const f32x4*)(term + i + k);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const float y = widen(x[g], k + q, nil);
-                const float f = y > 0.f ? down : up;
-                z[k + q] = ((rep >> (g * E + k + q)) & 1 ? y * f : y) + t[q];
-              }
-            }
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              const uint32_t sel = select_word(h, d, nil);
-              const uint32_t w = x[g][d];
-              x[g][d] = (round_word(z, d, nil) & sel) | (w & ~sel);
-            }
-          }
-          if (mk[g] != kAll) {
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              const uint32_t sel = select_word(mk[g], d, nil);
-              const uint32_t w = x[g][d];
-              x[g][d] = (w & sel) | (kMinusInf<T> & ~sel);
-            }
-          }
-          T* p = out + r * a.out_row + i;
-          if (i + E <= left) {
-            ((Vec16b*)p)->v = x[g];
-          } else {
-            T t[E];
-            __builtin_memcpy(t, &x[g], 16);
-#pragma unroll
-            for (int k = 0; k < E; ++k)
-              if (i + k < left) p[k] = t[k];
-          }
-        }
-        mk[g] = next[g];
+        for (int k = 0; k < E; ++k)
+          if (i + k < left) p[k] = t[k];
       }
     }
+    mk = next;
+    ++r;
   }
 }
 
 template <typename T, bool kInPlace>
 void launch(AdjustArgs a, hipStream_t st) {
   constexpr int G = SV_ADJUST_GROUPS * (int)sizeof(T) / 2, kTile = G * Lanes<T>::kGroup;
-  a.n_tiles = (a.V + kTile - 1) / kTile;
+  const int64_t tiles = (a.V + kTile - 1) / kTile;
   // rows go to several waves where a wave per tile would leave the card idle
-  const int64_t tiles = (int64_t)a.B * a.n_tiles;
-  int64_t chunks = (kWantedWaves + tiles - 1) / tiles;
+  int64_t chunks = (kWantedWaves + tiles * a.B - 1) / (tiles * a.B);
   chunks = chunks < a.R ? chunks : a.R;
   a.chunk = (int)((a.R + chunks - 1) / chunks);
-  a.n_chunks = (a.R + a.chunk - 1) / a.chunk;
-  const int64_t groups = (tiles * a.n_chunks + kWaves - 1) / kWaves;
-  const unsigned grid = (unsigned)(groups < kMaxGroups ? groups : kMaxGroups);
-  hipLaunchKernelGGL((k_adjust<T, G, kInPlace>), dim3(grid), dim3(kWaves * kWave), 0, st, a);
+  chunks = (a.R + a.chunk - 1) / a.chunk;
+  for (a.b0 = 0; a.b0 < a.B; a.b0 += kGridY) {
+    const dim3 grid((unsigned)((tiles + kWaves - 1) / kWaves),
+                    a.B - a.b0 < kGridY ? a.B - a.b0 : kGridY, (unsigned)chunks);
+    hipLaunchKernelGGL((k_adjust<T, G, kInPlace>), grid, dim3(kWaves * kWave), 0, st, a);
+  }
 }
 
 }  // namespace
