@@ -53,6 +53,7 @@ extern "C" {
 #define SV_V_MAX (1 << 24)   /* largest vocabulary accepted */
 #define SV_B_MAX (1 << 21)   /* most sessions per call */
 #define SV_SLOTS_MAX (1 << 25) /* most row slots B * (2M + 1) per call */
+#define SV_BIAS_MAX (1 << 30)  /* most bias entries per call */
 
 /* Per-session sampling profile (SDCP Sec. 4.1 "sampling"), 24 bytes,
  * 8-byte aligned; passed as a DEVICE array [B]. */

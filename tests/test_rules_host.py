@@ -61,7 +61,8 @@ def adjust(logits=FAKE, ss=30, rs=10, dtype=0, tokens=FAKE, m=FAKE, pen=FAKE, hi
     h = {"ok": sv._History(FAKE, FAKE, 2), "null": sv._History(None, FAKE, 2),
          "none": sv._History(FAKE, FAKE, 0), "few": sv._History(FAKE, FAKE, 1)}.get(hist, hist)
     b = {"ok": sv._Bias(FAKE, FAKE, FAKE, 3), "null": sv._Bias(None, FAKE, FAKE, 3),
-         "ids": sv._Bias(FAKE, None, FAKE, 3), "neg": sv._Bias(FAKE, FAKE, FAKE, -1)}.get(bias, bias)
+         "ids": sv._Bias(FAKE, None, FAKE, 3), "neg": sv._Bias(FAKE, FAKE, FAKE, -1),
+         "long": sv._Bias(FAKE, FAKE, FAKE, (1 << 30) + 1)}.get(bias, bias)
     k = {"ok": sv._Masks(FAKE, FAKE, 1), "null": sv._Masks(FAKE, None, 1),
          "none": sv._Masks(FAKE, FAKE, 0)}.get(masks, masks)
     ptr = lambda x: None if x is None else ctypes.byref(x)  # noqa: E731
@@ -74,7 +75,7 @@ def adjust(logits=FAKE, ss=30, rs=10, dtype=0, tokens=FAKE, m=FAKE, pen=FAKE, hi
     dict(M=-1, R=1), dict(M=65, R=65), dict(R=0, M=0), dict(R=4), dict(R=1), dict(V=0),
     dict(V=(1 << 24) + 1), dict(ss=-1), dict(rs=-1), dict(ss=(1 << 40) + 1), dict(tokens=None),
     dict(hist="null"), dict(hist="none"), dict(hist="few", slots=None), dict(bias="null"),
-    dict(bias="ids"), dict(bias="neg"), dict(masks="null"), dict(masks="none")],
+    dict(bias="ids"), dict(bias="neg"), dict(bias="long"), dict(masks="null"), dict(masks="none")],
     ids=lambda d: ",".join(f"{k}={v}" for k, v in d.items()))
 def test_adjust_refuses(bad):
     assert adjust(**bad) == sv.ERR_ARG

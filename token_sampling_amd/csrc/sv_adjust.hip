@@ -7,6 +7,7 @@
 //   z = z - freq * c - (c > 0 ? pres : 0) + bias(v)
 //   z = mask bit clear ? -inf : z
 // in binary32, rounded once to the logits' type.
+#include <limits.h>
 #include <math.h>
 
 #include "sv_common.hpp"
@@ -14,20 +15,9 @@
 namespace sv {
 namespace {
 
-#ifndef SV_ADJUST_WAVES
-#define SV_ADJUST_WAVES 4
-#endif
-constexpr int kWaves = SV_ADJUST_WAVES;  // per workgroup; each works by itself
-constexpr int64_t kWantedWaves = 8192;   // two for each place of a wave in the card's SIMDs
-constexpr int kGridY = 32768;  // sessions of a launch
-constexpr int kScan = 4;       // 64s of biases that a wave looks through without a search
-#ifndef SV_ADJUST_BATCH
-#define SV_ADJUST_BATCH 4
-#endif
-constexpr int kBatch = SV_ADJUST_BATCH;  // rows in flight together
-#ifndef SV_ADJUST_GROUPS
-#define SV_ADJUST_GROUPS 2
-#endif
+constexpr int64_t kWantedWaves = 8192;  // two for each place of a wave in the card's SIMDs
+constexpr int kGridY = 32768;           // sessions of a launch
+constexpr int kBatch = 4;               // logits of a lane in flight, in place
 
 struct AdjustArgs {
   const void* logits;
@@ -54,26 +44,14 @@ struct AdjustArgs {
   int32_t* status;
 };
 
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-struct __attribute__((packed, aligned(2))) Vec16b {
-  u32x4 v;
-};
-
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4), may_alias));
+// a vector at any logit's address
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2), may_alias));
 __device__ inline u32x4 load16(const void* p) {
-#if SV_NT & 1
-  typedef unsigned int uu __attribute__((ext_vector_type(4), aligned(2)));
-  return __builtin_nontemporal_load((const uu*)p);
-#else
-  return ((const Vec16b*)p)->v;
-#endif
+  return __builtin_nontemporal_load((const u32x4_any*)p);
 }
 __device__ inline void store16(void* p, u32x4 v) {
-#if SV_NT & 2
-  typedef unsigned int uu __attribute__((ext_vector_type(4), aligned(2)));
-  __builtin_nontemporal_store((uu)v, (uu*)p);
-#else
-  ((Vec16b*)p)->v = v;
-#endif
+  __builtin_nontemporal_store((u32x4_any)v, (u32x4_any*)p);
 }
 
 // A lane's share of a row: one 16-byte vector per group, 8 bf16 or 4 binary32
@@ -142,22 +120,21 @@ __device__ inline Session session_of(const AdjustArgs& a, int b) {
   return s;
 }
 
-// The first entry of ids[lo, hi) that is not below v, found by the wave: 64
-// probes a step.
-__device__ inline int lower_bound(const int32_t* ids, int lo, int hi, int v) {
-  const int lane = __lane_id();
-  while (lo < hi) {
+// Narrows ascending ids[lo, hi) to a range with every id of [v, v + n): 64
+// probes, which tell the entries before the last probe below v and after the
+// first one not below v + n, as often as that halves the range.
+__device__ inline void narrow(const int32_t* ids, int& lo, int& hi, int v, int n) {
+  while (hi - lo > kWave) {
     const int step = (hi - lo + kWave - 1) / kWave;
-    const int64_t at = (int64_t)lo + (int64_t)lane * step;
-    // probes are ascending: those below v come first
-    const int below = __popcll(__ballot(at < hi && ids[at] < v));
-    if (step == 1) return lo + below;
-    if (below == 0) return lo;
-    const int64_t end = (int64_t)lo + (int64_t)below * step;
-    lo = lo + (below - 1) * step + 1;
-    hi = end < hi ? (int)end : hi;
+    const int64_t at = lo + (int64_t)__lane_id() * step;
+    const int id = at < hi ? ids[at] : INT_MAX;
+    const int below = __popcll(__ballot(id < v)), upto = __popcll(__ballot(id < v + n));
+    const int64_t end = lo + (int64_t)upto * step;
+    const int was = hi - lo;
+    if (below > 0) lo += (below - 1) * step + 1;
+    if (end < hi) hi = (int)end;
+    if (hi - lo > was / 2) return;
   }
-  return lo;
 }
 
 // All ones where bit i of bits is set, else zeros.
@@ -188,35 +165,40 @@ constexpr uint32_t kHad = 0x2000;   // output before: its presence is counted
 constexpr uint32_t kOn = 0x4000;    // a rule changes it (not yet, for a drafted token ahead)
 constexpr uint32_t kBias = 0x8000;  // it has a bias
 
-// One wave works on one unit: kTile neighbouring tokens of one session, row
-// after row.  What the rows share is set up once, in the wave's own LDS: the
-// list of the tokens that the history, a bias or a drafted token touches, and
-// an additive term for each.  Then the rows stream in 16-byte vectors, a few
-// thousand tokens a row out of 1e5 passing through LDS on the way, where one
-// lane a listed token changes them: with every lane working out its own
-// vector's changes instead, a wave took 200 vector instructions a row and tile
-// and the kernel was bound by them in place.  Vectors with an empty mask are
-// not read; in place, rows without a mask move their listed tokens alone.
-template <typename T, int G, bool kInPlace>
-__global__ __launch_bounds__(kWaves* kWave) void k_adjust(AdjustArgs a) {
+// One wave, a workgroup of its own, works on kTile neighbouring tokens of one
+// session, row after row.  What the rows share is set up once, in LDS: the list
+// of the tokens that the history, a bias or a drafted token touches, and an
+// additive term for each.  Then the rows stream in 16-byte vectors, the next
+// row's on the way while this one is worked on; vectors that hold listed tokens
+// pass through LDS, where one lane a listed token changes it, and vectors with
+// an empty mask are not read.  In place, rows without a mask move their listed
+// tokens alone, lanes spread over tokens and rows.
+//
+// What bounds it: out of place, HBM (188 us at B=256, M=8, V=128256 bf16 with
+// every rule: 1.2 GB at 6.3 TB/s; 61 us for one binary32 row of 256 sessions,
+// V=129280).  In place, the same sessions without masks take 98 us for 0.18 GB
+// of scattered 64-byte pieces, and the chain of dependent loads (controls,
+// history bits, counts, logits) of about 8 us a wave.
+// Why so: lanes that each work out their own vector's changes take 200 vector
+// instructions a row and tile against 60 here, which bound the kernel in place;
+// with workgroups of four waves, LDS stays held until the last one ends (253
+// and 202 us of then); loads and stores are non-temporal because the rows are
+// met once (198 and 188 us; the acceptance step that reads them afterwards is
+// 15% faster too).
+template <typename T, int G, bool kInPlace, bool kMasks>
+__global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
   using L = Lanes<T>;
   constexpr int E = L::kE, kTile = G * L::kGroup;
   constexpr uint32_t kAll = (1u << E) - 1;  // one vector's tokens
   constexpr uint32_t kFull = G * E == 32 ? ~0u : (1u << (G * E)) - 1;
   static_assert(G * E <= 32 && kTile <= (int)kPlace + 1, "a lane's tokens fit one word");
-  __shared__ __attribute__((aligned(16))) T lds_raw[kWaves][kTile];
-  __shared__ float lds_term[kWaves][kTile];
-  __shared__ uint16_t lds_list[kWaves][kTile];
-  __shared__ uint32_t lds_bits[kWaves][kTile / 32];
+  constexpr bool kVectors = !kInPlace || kMasks;  // whole vectors move
+  __shared__ __attribute__((aligned(16))) T raw[kVectors ? kTile : 1];
+  __shared__ float term[kTile];
+  __shared__ uint16_t list[kTile];
+  __shared__ uint32_t bits[kTile / 32];
   const int lane = __lane_id();
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  T* raw = lds_raw[wave];
-  float* term = lds_term[wave];
-  uint16_t* list = lds_list[wave];
-  uint32_t* bits = lds_bits[wave];
-  const int tile = blockIdx.x * kWaves + wave;
-  const int v0 = tile * kTile;
-  if (v0 >= a.V) return;
+  const int tile = blockIdx.x, v0 = tile * kTile;
   const int first = lane * E;   // a lane's vectors start at first + g * kGroup
   const int left = a.V - v0;    // tokens from the tile's start to the row's end
   const int chunk = blockIdx.z;
@@ -263,7 +245,7 @@ __global__ __launch_bounds__(kWaves* kWave) void k_adjust(AdjustArgs a) {
     return w & within;
   };
   auto mask_row = [&](int r) {
-    if (a.mask_rows == nullptr || r >= r1) return -1;
+    if (!kMasks || r >= r1) return -1;
     return r < kWave ? lane_read(s.mask_row, r) : s.mask_row64;
   };
   auto mask_of = [&](int k) {
@@ -298,21 +280,12 @@ __global__ __launch_bounds__(kWaves* kWave) void k_adjust(AdjustArgs a) {
   const int mask0 = mask_row(r0);
   if (mask0 >= 0) mask = bytes_of(a.mask_bits + (size_t)mask0 * a.W);
   int bias_lo = s.bias_lo, bias_hi = s.bias_hi;
-  if (bias_hi - bias_lo > kScan * kWave) {
-    bias_lo = lower_bound(a.bias_id, bias_lo, bias_hi, v0);
-    bias_hi = lower_bound(a.bias_id, bias_lo, bias_hi, v0 + kTile);
-  }
-  int32_t id[kScan];
-  float bias[kScan];
-#pragma unroll
-  for (int c = 0; c < kScan; ++c) {
-    const int e = bias_lo + c * kWave + lane;
-    id[c] = -1;
-    bias[c] = 0.f;
-    if (e < bias_hi) {
-      id[c] = a.bias_id[e];
-      bias[c] = a.bias_val[e];
-    }
+  narrow(a.bias_id, bias_lo, bias_hi, v0, kTile);
+  int32_t id = -1;
+  float bias = 0.f;
+  if (bias_lo + lane < bias_hi) {
+    id = a.bias_id[bias_lo + lane];
+    bias = a.bias_val[bias_lo + lane];
   }
   u32x4 x[G];
   uint32_t mk = mask0 < 0 ? kFull : packed(mask);
@@ -323,21 +296,19 @@ __global__ __launch_bounds__(kWaves* kWave) void k_adjust(AdjustArgs a) {
   const uint64_t mine = __ballot(s.token >= v0 && s.token - v0 < kTile && lane < r1 - 1);
   uint32_t biased = 0, any = rep;
   auto here = [&](int v) { return v >= v0 && v < a.V && v - v0 < kTile; };
-  bool biases = bias_hi - bias_lo > kScan * kWave;
-#pragma unroll
-  for (int c = 0; c < kScan; ++c) biases |= here(id[c]);
-  if (mine != 0 || __any(biases)) {
-    if (lane < kTile / 32) bits[lane] = 0;
+  if (mine != 0 || __any(here(id)) || bias_hi - bias_lo > kWave) {
+    for (int w = lane; w < kTile / 32; w += kWave) bits[w] = 0;
     wave_sync();
-    auto note = [&](int v, float t) {
-      if (!here(v)) return;
-      atomicOr(bits + (v - v0) / 32, 1u << ((v - v0) % 32));
-      term[v - v0] = t;
-    };
-#pragma unroll
-    for (int c = 0; c < kScan; ++c) note(id[c], bias[c]);
-    for (int e = bias_lo + kScan * kWave + lane; e < bias_hi; e += kWave)
-      note(a.bias_id[e], a.bias_val[e]);
+    for (int e = bias_lo + lane; e < bias_hi; e += kWave) {
+      if (e != bias_lo + lane) {
+        id = a.bias_id[e];
+        bias = a.bias_val[e];
+      }
+      if (here(id)) {
+        atomicOr(bits + (id - v0) / 32, 1u << ((id - v0) % 32));
+        term[id - v0] = bias;
+      }
+    }
     wave_sync();
     auto noted = [&] {
       uint32_t w = 0;
@@ -405,7 +376,7 @@ __global__ __launch_bounds__(kWaves* kWave) void k_adjust(AdjustArgs a) {
 
   for (int r = r0; r < r1;) {
     if (r > r0 && ((mine >> (r - 1)) & 1)) meet(r - 1);
-    if (kInPlace && mask_row(r) < 0) {
+    if (!kVectors || (kInPlace && mask_row(r) < 0)) {
       // rows alike: up to the next that meets a token of this tile or has a mask
       int n = r1 - r;
       const uint64_t met = r < kWave ? mine >> r : 0, held = r < kWave ? masked >> r : 0;
@@ -434,64 +405,66 @@ __global__ __launch_bounds__(kWaves* kWave) void k_adjust(AdjustArgs a) {
       r += n;
       continue;
     }
-    const uint32_t next = mask_of(mask_row(r + 1));
-    // in place: the vectors that change (any has a bit for each listed token)
-    if constexpr (kInPlace) {
-      mk = mask_of(mask_row(r));
-      load(r, mk, any | (mk ^ kFull), x);
-    }
-    u32x4 y[G];
-#pragma unroll
-    for (int g = 0; g < G; ++g) y[g] = x[g];
-    if constexpr (!kInPlace) {
-      if (r + 1 < r1) load(r + 1, next, kFull, x);
-    }
-    if (listed > 0) {
-#pragma unroll
-      for (int g = 0; g < G; ++g)
-        if ((any >> (g * E)) & kAll) *(u32x4*)(raw + g * L::kGroup + first) = y[g];
-      wave_sync();
-      for (int j = lane; j < listed; j += kWave) {
-        const uint32_t e = list[j];
-        const int i = e & kPlace;
-        if (e & kOn) raw[i] = (T)changed((float)raw[i], e, term[i]);
+    if constexpr (kVectors) {
+      const uint32_t next = mask_of(mask_row(r + 1));
+      // in place: the vectors that change (any has a bit for each listed token)
+      if constexpr (kInPlace) {
+        mk = mask_of(mask_row(r));
+        load(r, mk, any | (mk ^ kFull), x);
       }
-      wave_sync();
+      u32x4 y[G];
 #pragma unroll
-      for (int g = 0; g < G; ++g)
-        if ((any >> (g * E)) & kAll) y[g] = *(const u32x4*)(raw + g * L::kGroup + first);
-    }
+      for (int g = 0; g < G; ++g) y[g] = x[g];
+      if constexpr (!kInPlace) {
+        if (r + 1 < r1) load(r + 1, next, kFull, x);
+      }
+      if (listed > 0) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int i = g * L::kGroup + first;
-      const uint32_t ok = (mk >> (g * E)) & kAll;
-      if (i >= left || (kInPlace && ((any >> (g * E)) & kAll) == 0 && ok == kAll)) continue;
-      if (ok != kAll) {
+        for (int g = 0; g < G; ++g)
+          if ((any >> (g * E)) & kAll) *(u32x4*)(raw + g * L::kGroup + first) = y[g];
+        wave_sync();
+        for (int j = lane; j < listed; j += kWave) {
+          const uint32_t e = list[j];
+          const int i = e & kPlace;
+          if (e & kOn) raw[i] = (T)changed((float)raw[i], e, term[i]);
+        }
+        wave_sync();
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          const uint32_t sel = select_word(ok, d, T(0)), w = y[g][d];
-          y[g][d] = (w & sel) | (kMinusInf<T> & ~sel);
+        for (int g = 0; g < G; ++g)
+          if ((any >> (g * E)) & kAll) y[g] = *(const u32x4*)(raw + g * L::kGroup + first);
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int i = g * L::kGroup + first;
+        const uint32_t ok = (mk >> (g * E)) & kAll;
+        if (i >= left || (kInPlace && ((any >> (g * E)) & kAll) == 0 && ok == kAll)) continue;
+        if (ok != kAll) {
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            const uint32_t sel = select_word(ok, d, T(0)), w = y[g][d];
+            y[g][d] = (w & sel) | (kMinusInf<T> & ~sel);
+          }
+        }
+        T* p = out + r * a.out_row + i;
+        if (i + E <= left) {
+          store16(p, y[g]);
+        } else {
+          T t[E];
+          __builtin_memcpy(t, &y[g], 16);
+#pragma unroll
+          for (int k = 0; k < E; ++k)
+            if (i + k < left) p[k] = t[k];
         }
       }
-      T* p = out + r * a.out_row + i;
-      if (i + E <= left) {
-        store16(p, y[g]);
-      } else {
-        T t[E];
-        __builtin_memcpy(t, &y[g], 16);
-#pragma unroll
-        for (int k = 0; k < E; ++k)
-          if (i + k < left) p[k] = t[k];
-      }
+      mk = next;
+      ++r;
     }
-    mk = next;
-    ++r;
   }
 }
 
-template <typename T, bool kInPlace>
+template <typename T, int kSize, bool kInPlace, bool kMasks>
 void launch(AdjustArgs a, hipStream_t st) {
-  constexpr int G = SV_ADJUST_GROUPS * (int)sizeof(T) / 2, kTile = G * Lanes<T>::kGroup;
+  constexpr int G = kSize * (int)sizeof(T) / 2, kTile = G * Lanes<T>::kGroup;
   const int64_t tiles = (a.V + kTile - 1) / kTile;
   // rows go to several waves where a wave per tile would leave the card idle
   int64_t chunks = (kWantedWaves + tiles * a.B - 1) / (tiles * a.B);
@@ -499,9 +472,32 @@ void launch(AdjustArgs a, hipStream_t st) {
   a.chunk = (int)((a.R + chunks - 1) / chunks);
   chunks = (a.R + a.chunk - 1) / a.chunk;
   for (a.b0 = 0; a.b0 < a.B; a.b0 += kGridY) {
-    const dim3 grid((unsigned)((tiles + kWaves - 1) / kWaves),
-                    a.B - a.b0 < kGridY ? a.B - a.b0 : kGridY, (unsigned)chunks);
-    hipLaunchKernelGGL((k_adjust<T, G, kInPlace>), grid, dim3(kWaves * kWave), 0, st, a);
+    const dim3 grid((unsigned)tiles, a.B - a.b0 < kGridY ? a.B - a.b0 : kGridY, (unsigned)chunks);
+    hipLaunchKernelGGL((k_adjust<T, G, kInPlace, kMasks>), grid, dim3(kWave), 0, st, a);
+  }
+}
+
+// One vector of a row per lane, or two.  One lets twice the waves share the LDS:
+// 54.7 against 60.5 us at B=128, R=17, V=32000 and 176 against 182 us at
+// V=128256 (bf16, penalties and masks).  Where rows start off a 16-byte
+// boundary every tile's ends share cache lines with its neighbours', and two
+// vectors have half as many ends: 208 against 221 us at V=128255.
+template <typename T>
+void launch(const AdjustArgs& a, hipStream_t st) {
+  constexpr int E = Lanes<T>::kE;
+  const bool even = (uintptr_t)a.logits % 16 == 0 && (uintptr_t)a.out % 16 == 0 &&
+                    a.in_session % E == 0 && a.in_row % E == 0 && a.out_session % E == 0 &&
+                    a.out_row % E == 0;
+  const bool many = (int64_t)a.B * a.V > kWantedWaves * Lanes<T>::kGroup;
+  if (a.out == a.logits) {
+    if (a.mask_rows) launch<T, 1, true, true>(a, st);
+    else launch<T, 1, true, false>(a, st);
+  } else if (many && !even) {
+    if (a.mask_rows) launch<T, 2, false, true>(a, st);
+    else launch<T, 2, false, false>(a, st);
+  } else {
+    if (a.mask_rows) launch<T, 1, false, true>(a, st);
+    else launch<T, 1, false, false>(a, st);
   }
 }
 
@@ -527,7 +523,7 @@ extern "C" int sv_adjust_logits(const void* logits, int64_t session_stride, int6
   if (history && (!history->counts || !history->seen || history->n_slots < 1 ||
                   (!slots && history->n_slots < B)))
     return SV_ERR_ARG;
-  if (bias && (!bias->offsets || bias->n < 0 || (bias->n > 0 && (!bias->ids || !bias->values))))
+  if (bias && (!bias->offsets || bias->n < 0 || bias->n > SV_BIAS_MAX || (bias->n > 0 && (!bias->ids || !bias->values))))
     return SV_ERR_ARG;
   if (masks && (!masks->bits || !masks->rows || masks->n_masks < 1)) return SV_ERR_ARG;
   AdjustArgs a = {};
@@ -565,12 +561,7 @@ extern "C" int sv_adjust_logits(const void* logits, int64_t session_stride, int6
   a.W = (V + 31) / 32;
   a.status = status;
   (void)hipGetLastError();
-  if (dtype == SV_BF16) {
-    if (in_place) launch<__bf16, true>(a, (hipStream_t)stream);
-    else launch<__bf16, false>(a, (hipStream_t)stream);
-  } else {
-    if (in_place) launch<float, true>(a, (hipStream_t)stream);
-    else launch<float, false>(a, (hipStream_t)stream);
-  }
+  if (dtype == SV_BF16) launch<__bf16>(a, (hipStream_t)stream);
+  else launch<float>(a, (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_DEVICE;
 }
