@@ -661,22 +661,37 @@ def make_vocab(tokens, end=(), device="cuda"):
                  torch.tensor(end, dtype=torch.int32).to(device))
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _launch(dev, stream):
     """(stream handle, context): the call's stream, and a context in which the
     tensors' device is current and new tensors belong to that stream."""
     import torch
 
-    here = torch.cuda.current_stream(dev)
-    if stream is None or stream.cuda_stream == here.cuda_stream:
-        stream, on = here, contextlib.nullcontext()
+    if dev.index == torch.cuda.current_device():
+        here = torch._C._cuda_getCurrentRawStream(dev.index)
+        if stream is None or stream.cuda_stream == here:
+            return here, _HERE
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    both = contextlib.ExitStack()
+    both.enter_context(torch.cuda.device(dev))
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
     else:
-        on = torch.cuda.stream(stream)
-    if dev.index is not None and dev.index != torch.cuda.current_device():
-        both = contextlib.ExitStack()
-        both.enter_context(torch.cuda.device(dev))
-        both.enter_context(on)
-        on = both
-    return stream.cuda_stream, on
+        both.enter_context(torch.cuda.stream(stream))
+    return stream.cuda_stream, both
+
+
+def _want(t, name, dtype, shape, device):
+    """_check, quick where t is as it should be: these calls are short enough on
+    the GPU for the host's checks to count."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _check(t, name, dtype, shape, device)
 
 
 def _device_of(t, name):
@@ -697,8 +712,8 @@ def _history_struct(history, V, dev):
     import torch
 
     n = history.counts.shape[0]
-    _check(history.counts, "history.counts", torch.int32, (n, V), dev)
-    _check(history.seen, "history.seen", torch.int32, (n, 2, (V + 31) // 32), dev)
+    _want(history.counts, "history.counts", torch.int32, (n, V), dev)
+    _want(history.seen, "history.seen", torch.int32, (n, 2, (V + 31) // 32), dev)
     return _History(history.counts.data_ptr(), history.seen.data_ptr(), n)
 
 
@@ -723,7 +738,7 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
     import torch
 
     dev = _device_of(logits, "logits")
-    if logits.dim() != 3 or 0 in logits.shape:
+    if logits.dim() != 3 or logits.numel() == 0:
         raise ValueError("logits must be a [B, R, V] tensor")
     B, R, V = logits.shape
     if logits.dtype == torch.bfloat16:
@@ -743,31 +758,31 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
             raise ValueError("m needs tokens")
     else:
         M = R - 1 if tokens.dim() == 2 and tokens.shape[1] == R - 1 else R
-        _check(tokens, "tokens", torch.int32, (B, M), dev)
+        _want(tokens, "tokens", torch.int32, (B, M), dev)
         if m is not None:
-            _check(m, "m", torch.int32, (B,), dev)
+            _want(m, "m", torch.int32, (B,), dev)
     if penalties is not None:
-        _check(penalties, "penalties", torch.uint8, (B, 16), dev)
+        _want(penalties, "penalties", torch.uint8, (B, 16), dev)
     hist = bs = mk = None
     if history is not None:
         hist = ctypes.byref(_history_struct(history, V, dev))
         if slots is None and history.counts.shape[0] < B:
             raise ValueError("history has fewer slots than sessions")
     if slots is not None:
-        _check(slots, "slots", torch.int32, (B,), dev)
+        _want(slots, "slots", torch.int32, (B,), dev)
     if bias is not None:
         n = bias.ids.numel()
-        _check(bias.offsets, "bias.offsets", torch.int32, (B + 1,), dev)
-        _check(bias.ids, "bias.ids", torch.int32, (n,), dev)
-        _check(bias.values, "bias.values", torch.float32, (n,), dev)
+        _want(bias.offsets, "bias.offsets", torch.int32, (B + 1,), dev)
+        _want(bias.ids, "bias.ids", torch.int32, (n,), dev)
+        _want(bias.values, "bias.values", torch.float32, (n,), dev)
         bs = ctypes.byref(_Bias(bias.offsets.data_ptr(), bias.ids.data_ptr(),
                                 bias.values.data_ptr(), n))
     if (masks is None) != (mask_rows is None):
         raise ValueError("masks and mask_rows go together")
     if masks is not None:
         n = masks.shape[0]
-        _check(masks, "masks", torch.int32, (n, (V + 31) // 32), dev)
-        _check(mask_rows, "mask_rows", torch.int32, (B, R), dev)
+        _want(masks, "masks", torch.int32, (n, (V + 31) // 32), dev)
+        _want(mask_rows, "mask_rows", torch.int32, (B, R), dev)
         if n < 1:
             raise ValueError("masks must hold a row")
         mk = ctypes.byref(_Masks(masks.data_ptr(), mask_rows.data_ptr(), n))
@@ -778,7 +793,7 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
         elif out is not logits and out.data_ptr() == logits.data_ptr() and out.stride() == (sb, sr, sv_):
             _check_like(out, logits)
         elif out is not logits:
-            _check(out, "out", logits.dtype, (B, R, V), dev)
+            _want(out, "out", logits.dtype, (B, R, V), dev)
             lo, hi = logits.data_ptr(), logits.data_ptr() + ((B - 1) * sb + (R - 1) * sr + V) * logits.element_size()
             if out.data_ptr() < hi and lo < out.data_ptr() + out.numel() * out.element_size():
                 raise ValueError("out overlaps logits")
@@ -790,7 +805,7 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
         if status is None:
             status = torch.empty(B, dtype=torch.int32, device=dev)
         else:
-            _check(status, "status", torch.int32, (B,), dev)
+            _want(status, "status", torch.int32, (B,), dev)
         rc = lib().sv_adjust_logits(logits.data_ptr(), sb, sr, dt, _ptr(tokens), _ptr(m),
                                     _ptr(penalties), hist, _ptr(slots), bs, mk, B, M, R, V,
                                     out.data_ptr(), status.data_ptr(), handle)
@@ -824,17 +839,17 @@ def count_tokens(history, tokens, slots=None, lens=None, offsets=None, prompt=Fa
         if lens is not None:
             raise ValueError("give lens or offsets, not both")
         B, L = offsets.numel() - 1, tokens.numel()
-        _check(tokens, "tokens", torch.int32, (L,), dev)
-        _check(offsets, "offsets", torch.int32, (B + 1,), dev)
+        _want(tokens, "tokens", torch.int32, (L,), dev)
+        _want(offsets, "offsets", torch.int32, (B + 1,), dev)
     else:
         if tokens.dim() != 2:
             raise ValueError("tokens must be [B, L] (or one line, with offsets)")
         B, L = tokens.shape
-        _check(tokens, "tokens", torch.int32, None, dev)
+        _want(tokens, "tokens", torch.int32, tokens.shape, dev)
         if lens is not None:
-            _check(lens, "lens", torch.int32, (B,), dev)
+            _want(lens, "lens", torch.int32, (B,), dev)
     if slots is not None:
-        _check(slots, "slots", torch.int32, (B,), dev)
+        _want(slots, "slots", torch.int32, (B,), dev)
     elif history.counts.shape[0] < B:
         raise ValueError("history has fewer slots than sessions")
     handle, on = _launch(dev, stream)
@@ -850,12 +865,12 @@ def _grammar_structs(grammar, vocab, dev):
 
     S, C = grammar.next.shape
     V = vocab.offsets.numel() - 1
-    _check(grammar.next, "grammar.next", torch.int32, (S, C), dev)
-    _check(grammar.classes, "grammar.classes", torch.uint8, (256,), dev)
-    _check(grammar.accept, "grammar.accept", torch.uint8, (S,), dev)
-    _check(vocab.bytes, "vocab.bytes", torch.uint8, (vocab.bytes.numel(),), dev)
-    _check(vocab.offsets, "vocab.offsets", torch.int32, (V + 1,), dev)
-    _check(vocab.end, "vocab.end", torch.int32, (vocab.end.numel(),), dev)
+    _want(grammar.next, "grammar.next", torch.int32, (S, C), dev)
+    _want(grammar.classes, "grammar.classes", torch.uint8, (256,), dev)
+    _want(grammar.accept, "grammar.accept", torch.uint8, (S,), dev)
+    _want(vocab.bytes, "vocab.bytes", torch.uint8, (vocab.bytes.numel(),), dev)
+    _want(vocab.offsets, "vocab.offsets", torch.int32, (V + 1,), dev)
+    _want(vocab.end, "vocab.end", torch.int32, (vocab.end.numel(),), dev)
     g = _Grammar(grammar.next.data_ptr(), grammar.classes.data_ptr(), grammar.accept.data_ptr(), S, C)
     v = _Vocab(vocab.bytes.data_ptr(), vocab.offsets.data_ptr(), vocab.end.data_ptr(),
                vocab.bytes.numel(), vocab.end.numel(), V)
@@ -870,13 +885,13 @@ def grammar_masks(grammar, vocab, states, out=None, stream=None):
     dev = _device_of(states, "states")
     g, v, V = _grammar_structs(grammar, vocab, dev)
     n = states.numel()
-    _check(states, "states", torch.int32, (n,), dev)
+    _want(states, "states", torch.int32, (n,), dev)
     handle, on = _launch(dev, stream)
     with on:
         if out is None:
             out = torch.empty((n, (V + 31) // 32), dtype=torch.int32, device=dev)
         else:
-            _check(out, "out", torch.int32, (n, (V + 31) // 32), dev)
+            _want(out, "out", torch.int32, (n, (V + 31) // 32), dev)
         rc = lib().sv_grammar_masks(g, v, states.data_ptr(), n, out.data_ptr(), handle)
     if rc != OK:
         raise SvError(f"sv_grammar_masks failed: {strerror(rc)} ({rc})")
@@ -896,18 +911,18 @@ def grammar_advance(grammar, vocab, states, tokens, lens=None, out=None, stream=
     if tokens.dim() != 2:
         raise ValueError("tokens must be [B, L]")
     B, L = tokens.shape
-    _check(tokens, "tokens", torch.int32, None, dev)
-    _check(states, "states", torch.int32, (B,), dev)
+    _want(tokens, "tokens", torch.int32, tokens.shape, dev)
+    _want(states, "states", torch.int32, (B,), dev)
     if lens is not None:
-        _check(lens, "lens", torch.int32, (B,), dev)
+        _want(lens, "lens", torch.int32, (B,), dev)
     handle, on = _launch(dev, stream)
     with on:
         if out is None:
             out = {"states": torch.empty((B, L + 1), dtype=torch.int32, device=dev),
                    "last": torch.empty(B, dtype=torch.int32, device=dev)}
         else:
-            _check(out["states"], "out['states']", torch.int32, (B, L + 1), dev)
-            _check(out["last"], "out['last']", torch.int32, (B,), dev)
+            _want(out["states"], "out['states']", torch.int32, (B, L + 1), dev)
+            _want(out["last"], "out['last']", torch.int32, (B,), dev)
         rc = lib().sv_grammar_advance(g, v, states.data_ptr(), tokens.data_ptr(), _ptr(lens), B, L,
                                       out["states"].data_ptr(), out["last"].data_ptr(), handle)
     if rc != OK:
