@@ -3,6 +3,8 @@
 //
 // A state s takes a byte c to next[s][classes[c]]; a token is the walk over its
 // bytes.  -1 stands for "no grammar" (and for a refused byte within a walk).
+#include <limits.h>
+
 #include <type_traits>
 
 #include "sv_common.hpp"
@@ -12,71 +14,118 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / kWave;
-constexpr int kHeld = 16;  // bytes of a token that a lane holds
+constexpr int kHeld = 16;  // first bytes of a token that are held
+constexpr int kMostEntries = 58880;  // of a table in LDS: 115 KB, and 45 KB for the tokens
 
 struct GrammarArgs {
   sv_grammar g;
   sv_vocab v;
 };
 
-// The automaton as the walks see it: each byte is a column, step(s, column) the
-// place after it.  Column stay() leaves every place (a token's end), column
-// refused() leads to the dead place from everywhere, as does a byte whose class
-// or next state lies outside the table; the dead place is never left.
+// The automaton as the walks see it: step(s, column) is the place after place s
+// and a byte of the column (class); the dead place, after a byte that is
+// refused, is never left.
 //
-// In LDS: rows of n_classes + 2 columns, the last row the dead place's, each
-// entry the start of the row it leads to, so that a step is an addition and a
-// 16-bit read.
-template <int kEntries>
+// In LDS: each entry is the start of the row it leads to, so that a step is an
+// addition and a 16-bit read; the dead place's row follows the states'.  With
+// kEnd there is one column more, end(), which stands for the end of a token and
+// leads from every state's place to the done place, the last row: places below
+// dead() are those of walks that go on.
+template <int kEntries, bool kEnd>
 struct Table {
   const uint16_t* t;
-  int classes, dead_;
-  static __host__ __device__ bool fits(const sv_grammar& g) {
-    return (int64_t)(g.n_states + 1ll) * (g.n_classes + 2) <= kEntries;
+  int width, dead_;
+  static bool fits(const sv_grammar& g) {
+    return g.n_classes < 256 && (g.n_states + (int64_t)2) * (g.n_classes + 1) <= kEntries;
   }
   __device__ Table(const sv_grammar& g, uint16_t* lds) : t(lds) {
-    classes = g.n_classes;
-    const int width = classes + 2;
+    const int classes = g.n_classes, total = g.n_states * classes;
+    width = classes + (kEnd ? 1 : 0);
     dead_ = g.n_states * width;
-    int s = threadIdx.x / width, c = threadIdx.x % width;
-    for (int i = threadIdx.x; i < dead_ + width; i += kThreads) {
-      int to = s;  // stay
-      if (c < classes && s < g.n_states) to = g.next[s * classes + c];
-      if (to < 0 || to > g.n_states || c > classes) to = g.n_states;
-      lds[i] = (uint16_t)(to * width);
-      s += kThreads / width;
-      c += kThreads % width;
-      if (c >= width) {
-        c -= width;
-        ++s;
+    // entry i of next, in row s and column c, is entry i + s here with kEnd; 16
+    // bytes of them a load, all loads of a pass before the first is used
+    const bool pieces = (uintptr_t)g.next % 16 == 0;
+    const int whole = pieces ? total / 4 : 0;
+    constexpr int kAhead = 4;
+    int s = 4 * threadIdx.x / classes, c = 4 * threadIdx.x % classes;
+    const int ds = 4 * kThreads / classes, dc = 4 * kThreads % classes;
+    auto put = [&](int i, int row, int to) {
+      lds[i + (kEnd ? row : 0)] = (uint16_t)(to >= 0 && to < g.n_states ? to * width : dead_);
+    };
+    for (int p0 = threadIdx.x; p0 < whole; p0 += kThreads * kAhead) {
+      int4 to[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int p = p0 + k * kThreads;
+        to[k] = ((const int4*)g.next)[p < whole ? p : p0];
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int i = 4 * (p0 + k * kThreads);
+        if (i < 4 * whole) {
+          int row = s, col = c;
+          auto next_column = [&] {
+            if (++col == classes) {
+              col = 0;
+              ++row;
+            }
+          };
+          put(i, row, to[k].x);
+          next_column();
+          put(i + 1, row, to[k].y);
+          next_column();
+          put(i + 2, row, to[k].z);
+          next_column();
+          put(i + 3, row, to[k].w);
+        }
+        s += ds;
+        c += dc;
+        if (c >= classes) {
+          c -= classes;
+          ++s;
+        }
       }
     }
+    for (int i = 4 * whole + threadIdx.x; i < total; i += kThreads) put(i, i / classes, g.next[i]);
+    if (threadIdx.x < (unsigned)width) lds[dead_ + threadIdx.x] = (uint16_t)dead_;
+    if constexpr (kEnd) {
+      const int done = dead_ + width;
+      for (int r = threadIdx.x; r < g.n_states; r += kThreads)
+        lds[r * width + classes] = (uint16_t)done;
+      if (threadIdx.x < (unsigned)width) lds[done + threadIdx.x] = (uint16_t)done;
+    }
   }
-  __device__ int stay() const { return classes; }
-  __device__ int refused() const { return classes + 1; }
   __device__ int dead() const { return dead_; }
-  __device__ int at(int state) const { return state * (classes + 2); }
-  __device__ int state(int place) const { return place / (classes + 2); }
+  __device__ int end() const { return width - 1; }
+  __device__ int at(int state) const { return state * width; }
+  __device__ int state(int place) const { return place / width; }
   __device__ int step(int s, int column) const { return t[s + column]; }
 };
 // In global memory, for automata that do not fit: places are states.
-template <>
-struct Table<0> {
+template <bool kEnd>
+struct Table<0, kEnd> {
   const int32_t* next;
   int states, classes;
   __device__ Table(const sv_grammar& g, uint16_t*)
       : next(g.next), states(g.n_states), classes(g.n_classes) {}
-  __device__ int stay() const { return classes; }
-  __device__ int refused() const { return classes + 1; }
   __device__ int dead() const { return -1; }
+  __device__ int end() const { return 0; }  // walks stop by the token's length here
   __device__ int at(int state) const { return state; }
   __device__ int state(int place) const { return place; }
   __device__ int step(int s, int column) const {
-    if (s < 0 || column == classes) return s;
-    const int to = column > classes ? -1 : next[(int64_t)s * classes + column];
-    return to >= 0 && to < states ? to : -1;
+    const int to = next[(int64_t)max(s, 0) * classes + column];
+    return s >= 0 && to >= 0 && to < states ? to : -1;
   }
 };
+
+// A byte's column, kRefused for a class outside the table.
+constexpr int kRefused = 0xFFFF;
+__device__ inline void columns_of(const sv_grammar& g, uint16_t* column) {
+  if (threadIdx.x < 256) {
+    const int c = g.classes[threadIdx.x];
+    column[threadIdx.x] = (uint16_t)(c < g.n_classes ? c : kRefused);
+  }
+}
 
 // Calls f(0), f(1), .. f(N - 1), each with its constant, until one returns false
 // (a loop around wave-wide votes is not unrolled, and an array that it indexes
@@ -87,21 +136,25 @@ __device__ inline void until(F&& f) {
     if (f(std::integral_constant<int, K>())) until<N, K + 1>(f);
 }
 
-// A token as a lane holds it: the columns of its first bytes, two to a word,
-// filled up with stay().
+// A token and its first bytes.
 struct Token {
-  int lo, len;  // its bytes; len = 0 for a token without any
+  int lo, len;  // its bytes; len = 0 for a token without any, or that ends a text
   bool end;     // it ends a text
-  uint32_t columns[kHeld / 2];
+  uint8_t bytes[kHeld];
 };
 
-template <typename TableT>
-__device__ inline Token token_of(const sv_vocab& v, const TableT& table, const uint16_t* column,
-                                 int id) {
-  Token t;
-  t.lo = 0;
-  t.len = 0;
-  t.end = false;
+// bytes[at] .. and up to kHeld - 1 more, n of them at least where there are so many.
+__device__ inline void held_bytes(const sv_vocab& v, int at, int n, uint8_t (&x)[kHeld]) {
+  if (at + kHeld <= v.n_bytes) {
+    __builtin_memcpy(x, v.bytes + at, kHeld);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) x[k] = k < n ? v.bytes[at + k] : 0;
+  }
+}
+
+__device__ inline Token token_of(const sv_vocab& v, int id) {
+  Token t = {};
   if (id >= 0 && id < v.V) {
     const int lo = v.offsets[id], hi = v.offsets[id + 1];
     t.lo = lo < 0 ? 0 : lo;
@@ -110,126 +163,216 @@ __device__ inline Token token_of(const sv_vocab& v, const TableT& table, const u
     for (int i = 0; i < v.n_end; ++i) t.end |= v.end[i] == id;
     if (t.end) t.len = 0;
   }
-  uint8_t x[kHeld] = {};
-  if (t.len > 0) {
-    if (t.lo + kHeld <= v.n_bytes) {
-      __builtin_memcpy(x, v.bytes + t.lo, kHeld);
-    } else {
-#pragma unroll
-      for (int k = 0; k < kHeld; ++k)
-        if (k < t.len) x[k] = v.bytes[t.lo + k];
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kHeld; k += 2) {
-    const uint32_t c0 = k < t.len ? column[x[k]] : table.stay();
-    const uint32_t c1 = k + 1 < t.len ? column[x[k + 1]] : table.stay();
-    t.columns[k / 2] = c0 | c1 << 16;
-  }
+  if (t.len > 0) held_bytes(v, t.lo, t.len, t.bytes);
   return t;
 }
 
-template <typename TableT>
-__device__ inline void columns_of(const sv_grammar& g, const TableT& table, uint16_t* column) {
-  if (threadIdx.x < 256) {
-    const int c = g.classes[threadIdx.x];
-    column[threadIdx.x] = (uint16_t)(c < g.n_classes ? c : table.refused());
-  }
-}
-
-// Masks of states k0 .. k0 + kStates - 1 over 1024 tokens: a unit of work.  Each
-// lane holds one token and takes it through kAbreast states at a time, whose
-// lookups overlap; a wave stops where none of its tokens goes on.  The ballots
-// are gathered in LDS and stored 128 bytes a state.
-constexpr int kStates = 64;
-#ifndef SV_ABREAST
-#define SV_ABREAST 4
-#endif
-constexpr int kAbreast = SV_ABREAST;
-static_assert(kStates % kAbreast == 0, "groups of states end with a unit");
+// Masks of states over a tile of kTile tokens, which a workgroup holds in LDS,
+// its tokens ordered by their first column.
+//
+// A state of a grammar mostly goes on from one byte in a hundred, so nearly all
+// walks would end at their first byte.  A wave takes one state at a time and
+// walks the tokens of the columns alone that the state goes on from, runs of
+// neighbouring columns together, 64 tokens abreast; those that are allowed set
+// their bit in the wave's words in LDS, which then go out whole.  Waves take
+// states as they become free, since some (inside a string) allow most tokens.
+// With a lane for each token and state instead, 1500 states over 128256 tokens
+// took 309 us, most of it on walks that ended at once.
+constexpr int kTile = 2048;
+constexpr int kStates = 512;   // states that a workgroup has at hand
+constexpr int kAbreast = 4;     // 64s of tokens whose lookups overlap
 template <int kEntries>
 __global__ __launch_bounds__(kThreads) void k_masks(GrammarArgs a, const int32_t* states, int n,
-                                                    int chunk, uint32_t* bits) {
+                                                    int part, uint32_t* bits) {
+  constexpr int kWords = kTile / 32, kEach = kTile / kThreads;
+  static_assert(kWords == kWave, "a word a lane");
   __shared__ uint16_t lds[kEntries ? kEntries : 1];
   __shared__ uint16_t column[256];
-  __shared__ uint64_t rows[kStates][kWaves];
-  __shared__ int32_t begin[kStates];  // the unit's states, -1 where every token is allowed
+  __shared__ __attribute__((aligned(16))) uint8_t columns[kTile][kHeld];
+  __shared__ uint16_t places[kTile];  // in the tile
+  __shared__ uint8_t lens[kEntries ? 1 : kTile];  // kHeld for longer ones; for walks without end()
+  __shared__ uint32_t words[kWaves][kWords];
+  __shared__ uint32_t ends[kWords];  // the tile's end tokens
+  constexpr int kLong = 256, kNone = 257;  // after the columns
+  __shared__ uint32_t begin[kNone + 1];  // where each column's tokens begin
+  __shared__ int32_t from_state[kStates];  // states in work, -1 where every token is allowed
   __shared__ bool accepts[kStates];
-  const Table<kEntries> table(a.g, lds);
-  columns_of(a.g, table, column);
-  __syncthreads();
+  __shared__ int next;  // the first that no wave has taken
+  const Table<kEntries, true> table(a.g, lds);
+  columns_of(a.g, column);
   const int lane = __lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int W = (a.v.V + 31) / 32;
-  const int chunks = (n + chunk - 1) / chunk, tiles = (a.v.V + kThreads - 1) / kThreads;
-  const int64_t units = (int64_t)tiles * chunks;
-  // a workgroup's units are neighbours: mostly the same tokens
-  const int64_t each = (units + gridDim.x - 1) / gridDim.x;
-  const int64_t u1 = (blockIdx.x + 1) * each < units ? (blockIdx.x + 1) * each : units;
-  int tile = -1, longest = 0;
-  Token t = {};
-  uint64_t valid = 0, ends = 0;
-  for (int64_t u = blockIdx.x * each; u < u1; ++u) {
-    if (tile != (int)(u / chunks)) {
-      tile = (int)(u / chunks);
-      const int id = tile * kThreads + (int)threadIdx.x;
-      t = token_of(a.v, table, column, id);
-      valid = __ballot(id < a.v.V);
-      ends = __ballot(t.end);
-      longest = wave_reduce(t.len, OpMax());
+  const int W = (a.v.V + 31) / 32, tile = blockIdx.x;
+  int k0 = blockIdx.y * part;
+  const int k1 = n - k0 < part ? n : k0 + part;
+  if (threadIdx.x <= kNone) begin[threadIdx.x] = 0;
+  if (threadIdx.x < kWords) ends[threadIdx.x] = 0;
+  __syncthreads();
+
+  // the tile's tokens by first column, then the long ones, then those that
+  // nothing allows (no bytes, or one that every state refuses)
+  {
+    if (threadIdx.x < (unsigned)a.v.n_end) {
+      const int i = a.v.end[threadIdx.x] - tile * kTile;
+      if (i >= 0 && i < kTile && i + tile * kTile < a.v.V) atomicOr(ends + i / 32, 1u << (i % 32));
     }
-    const int k0 = (int)(u % chunks) * chunk;
-    const int count = n - k0 < chunk ? n - k0 : chunk;
-    if (threadIdx.x < kStates) {
-      const int state = threadIdx.x < count ? states[k0 + threadIdx.x] : -1;
+    int lo[kEach], len[kEach], first[kEach];
+    uint8_t held[kEach][kHeld];
+    uint32_t rank[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int id = min(tile * kTile + e * kThreads + (int)threadIdx.x, a.v.V - 1);
+      lo[e] = a.v.offsets[id];
+      len[e] = a.v.offsets[id + 1];
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      lo[e] = max(lo[e], 0);
+      len[e] = min(len[e], a.v.n_bytes) - lo[e];
+      if (tile * kTile + e * kThreads + (int)threadIdx.x >= a.v.V) len[e] = 0;
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+      if (len[e] > 0) held_bytes(a.v, lo[e], len[e], held[e]);
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = e * kThreads + (int)threadIdx.x;
+      if ((ends[i / 32] >> (i % 32)) & 1) len[e] = 0;
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int c = k < len[e] ? column[held[e][k]] : table.end();
+        held[e][k] = (uint8_t)c;
+        if (c == kRefused) len[e] = 0;
+      }
+      first[e] = len[e] > kHeld ? kLong : len[e] > 0 ? held[e][0] : kNone;
+      rank[e] = atomicAdd(begin + first[e], 1u);
+    }
+    __syncthreads();
+    if (wave == 0) {
+      uint32_t before = 0;
+      for (int c0 = 0; c0 <= kNone; c0 += kWave) {
+        const uint32_t x = c0 + lane <= kNone ? begin[c0 + lane] : 0;
+        const uint32_t upto = wave_incl_scan(x);
+        if (c0 + lane <= kNone) begin[c0 + lane] = before + upto - x;
+        before += lane_read(upto, kWave - 1);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int p = begin[first[e]] + rank[e];
+      places[p] = (uint16_t)(e * kThreads + threadIdx.x);
+      if constexpr (!kEntries) lens[p] = (uint8_t)min(len[e], kHeld);
+      __builtin_memcpy(__builtin_assume_aligned(columns[p], 16), held[e], kHeld);
+    }
+    __syncthreads();
+  }
+
+  uint32_t* mine = words[wave];
+  const int w = tile * kWords + lane, left = a.v.V - w * 32;  // tokens from the lane's word on
+  const uint32_t valid = left < 32 ? (1u << (left > 0 ? left : 0)) - 1 : ~0u;
+
+  // N times 64 tokens from p on, those before p1, from state place from on
+  auto walk = [&](int from, int p, int p1, auto abreast, auto tails) {
+    constexpr int N = decltype(abreast)::value;
+    constexpr bool kTails = decltype(tails)::value;  // tokens longer than kHeld
+    int place[N], s[N];
+    [[maybe_unused]] int len[N];
+    uint32_t c[N][kHeld / 4];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int q = min(p + j * kWave + lane, p1 - 1);
+      __builtin_memcpy(c[j], __builtin_assume_aligned(columns[q], 16), kHeld);
+      place[j] = places[q];
+      if constexpr (!kEntries) len[j] = lens[q];
+      s[j] = p + j * kWave + lane < p1 ? from : table.dead();
+    }
+    until<kHeld>([&](auto k) {
+      bool live = false;
+      int least = INT_MAX;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        // (a branch here would keep the lookups from overlapping)
+        const int to = table.step(s[j], (c[j][k / 4] >> (8 * (k % 4))) & 0xFF);
+        if constexpr (kEntries) {
+          s[j] = to;
+          least = min(least, to);
+        } else {
+          s[j] = k < len[j] ? to : s[j];
+          live |= k + 1 < len[j] && s[j] != table.dead();
+        }
+      }
+      if constexpr (kEntries) live = least < table.dead();
+      return __any(live) != 0;
+    });
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (kTails && s[j] != table.dead()) {
+        const int id = tile * kTile + place[j];
+        const int at = max(a.v.offsets[id], 0), end = min(a.v.offsets[id + 1], a.v.n_bytes);
+        for (int b = at + kHeld; b < end && s[j] != table.dead(); b += kHeld) {
+          uint8_t y[kHeld];
+          int then[kHeld];
+          held_bytes(a.v, b, end - b, y);
+#pragma unroll
+          for (int k = 0; k < kHeld; ++k) then[k] = column[y[k]];
+#pragma unroll
+          for (int k = 0; k < kHeld; ++k) {
+            const int to = table.step(s[j], then[k] == kRefused ? 0 : then[k]);
+            if (k < end - b) s[j] = then[k] == kRefused ? table.dead() : to;
+          }
+        }
+      }
+      if (s[j] != table.dead()) atomicOr(mine + place[j] / 32, 1u << (place[j] % 32));
+    }
+  };
+
+  for (; k0 < k1; k0 += kStates) {
+    const int count = min(k1 - k0, kStates);
+    __syncthreads();
+    if (threadIdx.x < (unsigned)count) {
+      const int state = states[k0 + threadIdx.x];
       const bool in = state >= 0 && state < a.g.n_states;
-      begin[threadIdx.x] = in ? state : -1;
+      from_state[threadIdx.x] = in ? state : -1;
       accepts[threadIdx.x] = in && a.g.accept[state] != 0;
     }
+    if (threadIdx.x == 0) next = 0;
     __syncthreads();
-    for (int j0 = 0; j0 < count; j0 += kAbreast) {
-      int start[kAbreast], s[kAbreast];
-#pragma unroll
-      for (int q = 0; q < kAbreast; ++q) {
-        start[q] = __builtin_amdgcn_readfirstlane(begin[j0 + q]);
-        s[q] = start[q] >= 0 ? table.at(start[q]) : table.dead();
-      }
-      until<kHeld>([&](auto k) {
-        const int c = k % 2 ? t.columns[k / 2] >> 16 : t.columns[k / 2] & 0xFFFF;
-        bool live = false;
-#pragma unroll
-        for (int q = 0; q < kAbreast; ++q) {
-          s[q] = table.step(s[q], c);
-          live |= s[q] != table.dead();
-        }
-        return __any(live && k + 1 < t.len) != 0;
-      });
-      if (longest > kHeld) {
-        for (int k = kHeld; k < t.len; ++k) {
-          const int c = column[a.v.bytes[t.lo + k]];
-          bool live = false;
-#pragma unroll
-          for (int q = 0; q < kAbreast; ++q) {
-            s[q] = table.step(s[q], c);
-            live |= s[q] != table.dead();
+    for (;;) {
+      int k = 0;
+      if (lane == 0) k = atomicAdd(&next, 1);
+      k = __builtin_amdgcn_readfirstlane(k);
+      if (k >= count) break;
+      const int state = __builtin_amdgcn_readfirstlane(from_state[k]);
+      uint32_t x = valid;
+      if (state >= 0) {
+        const int from = table.at(state);
+        mine[lane] = 0;
+        for (int c0 = 0; c0 < a.g.n_classes; c0 += kWave) {
+          uint64_t on = __ballot(c0 + lane < a.g.n_classes &&
+                                 table.step(from, c0 + lane) != table.dead());
+          while (on != 0) {
+            const int lo = __builtin_ctzll(on);
+            const uint64_t rest = ~(on >> lo);
+            const int run = rest != 0 ? __builtin_ctzll(rest) : kWave - lo;
+            on = lo + run < kWave ? on & (~0ull << (lo + run)) : 0;
+            int p = __builtin_amdgcn_readfirstlane(begin[c0 + lo]);
+            const int p1 = __builtin_amdgcn_readfirstlane(begin[c0 + lo + run]);
+            for (; p1 - p > kWave; p += kAbreast * kWave)
+              walk(from, p, p1, std::integral_constant<int, kAbreast>(), std::false_type());
+            if (p < p1) walk(from, p, p1, std::integral_constant<int, 1>(), std::false_type());
           }
-          if (!live) break;
         }
+        const int tails = __builtin_amdgcn_readfirstlane(begin[kNone]);
+        for (int p = __builtin_amdgcn_readfirstlane(begin[kLong]); p < tails; p += kWave)
+          walk(from, p, tails, std::integral_constant<int, 1>(), std::true_type());
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        x = mine[lane] | (accepts[k] ? ends[lane] : 0);
       }
-#pragma unroll
-      for (int q = 0; q < kAbreast; ++q) {
-        uint64_t m = __ballot(s[q] != table.dead() && t.len > 0);
-        if (ends != 0 && accepts[j0 + q]) m |= ends;
-        if (start[q] < 0) m = valid;
-        if (lane == 0 && j0 + q < count) rows[j0 + q][wave] = m;
-      }
+      if (w < W) bits[(size_t)(k0 + k) * W + w] = x;
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < count * kWaves * 2; i += kThreads) {
-      const int j = i / (kWaves * 2), w = tile * (kThreads / 32) + i % (kWaves * 2);
-      if (w < W) bits[(size_t)(k0 + j) * W + w] = ((const uint32_t*)rows[j])[i % (kWaves * 2)];
-    }
-    __syncthreads();
   }
 }
 
@@ -241,8 +384,8 @@ __global__ __launch_bounds__(kThreads) void k_advance(GrammarArgs a, const int32
                                                       int B, int L, int32_t* out, int32_t* last) {
   __shared__ uint16_t lds[kEntries ? kEntries : 1];
   __shared__ uint16_t column[256];
-  const Table<kEntries> table(a.g, lds);
-  columns_of(a.g, table, column);
+  const Table<kEntries, false> table(a.g, lds);
+  columns_of(a.g, column);
   __syncthreads();
   const int lane = __lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -257,8 +400,12 @@ __global__ __launch_bounds__(kThreads) void k_advance(GrammarArgs a, const int32
   if (lane == 0) out[0] = in ? from : -1;
   for (int i0 = 0; i0 < L; i0 += kWave) {
     const int held = n - i0 < kWave ? n - i0 : kWave;  // may be 0 or less
-    const Token t =
-        token_of(a.v, table, column, lane < held ? tokens[(size_t)b * L + i0 + lane] : -1);
+    const Token t = token_of(a.v, lane < held ? tokens[(size_t)b * L + i0 + lane] : -1);
+    uint32_t columns[kHeld / 2];  // of its first bytes, two to a word
+#pragma unroll
+    for (int k = 0; k < kHeld; k += 2)
+      columns[k / 2] = column[t.bytes[k]] | (uint32_t)column[t.bytes[k + 1]] << 16;
+    auto step = [&](int c) { return c == kRefused ? table.dead() : table.step(s, c); };
     int mine = table.dead();
     for (int i = 0; i < held && s != table.dead(); ++i) {
       const int len = lane_read(t.len, i);
@@ -267,14 +414,17 @@ __global__ __launch_bounds__(kThreads) void k_advance(GrammarArgs a, const int32
         break;
       }
       until<kHeld>([&](auto k) {
-        const uint32_t c = lane_read(t.columns[k / 2], i);
-        s = table.step(s, k % 2 ? c >> 16 : c & 0xFFFF);
+        const uint32_t c = lane_read(columns[k / 2], i);
+        s = step(k % 2 ? c >> 16 : c & 0xFFFF);
         return k + 1 < len;
       });
       if (len > kHeld) {
         const int lo = lane_read(t.lo, i);
-        for (int k = kHeld; k < len && s != table.dead(); ++k)
-          s = table.step(s, column[a.v.bytes[lo + k]]);
+        for (int k0 = kHeld; k0 < len && s != table.dead(); k0 += kWave) {
+          // the next 64 bytes' columns, one a lane
+          const int c = k0 + lane < len ? column[a.v.bytes[lo + k0 + lane]] : kRefused;
+          for (int k = 0; k < kWave && k0 + k < len; ++k) s = step(lane_read(c, k));
+        }
       }
       s = __builtin_amdgcn_readfirstlane(s);
       if (lane == i) mine = s;
@@ -287,9 +437,8 @@ __global__ __launch_bounds__(kThreads) void k_advance(GrammarArgs a, const int32
 // Calls f with the LDS table size for g, 0 where none holds it.
 template <typename F>
 void by_size(const sv_grammar& g, F f) {
-  if (Table<8192>::fits(g)) f(std::integral_constant<int, 8192>());
-  else if (Table<32768>::fits(g)) f(std::integral_constant<int, 32768>());
-  else if (Table<65536>::fits(g)) f(std::integral_constant<int, 65536>());
+  if (Table<8192, true>::fits(g)) f(std::integral_constant<int, 8192>());
+  else if (Table<kMostEntries, true>::fits(g)) f(std::integral_constant<int, kMostEntries>());
   else f(std::integral_constant<int, 0>());
 }
 
@@ -314,14 +463,15 @@ extern "C" int sv_grammar_masks(const sv_grammar* grammar, const sv_vocab* vocab
   (void)hipGetLastError();
   by_size(*grammar, [&](auto entries) {
     constexpr int kEntries = decltype(entries)::value;
-    // units of up to kStates states for every workgroup that the card holds
-    const int64_t tiles = (vocab->V + kThreads - 1) / kThreads;
-    const int64_t places = kEntries > 32768 ? 256 : 512;
-    int64_t chunk = (n * tiles + places - 1) / places;
-    chunk = chunk < kAbreast ? kAbreast : chunk > kStates ? kStates : chunk;
-    const int64_t units = tiles * ((n + chunk - 1) / chunk);
-    hipLaunchKernelGGL(k_masks<kEntries>, dim3((unsigned)(units < places ? units : places)),
-                       dim3(kThreads), 0, (hipStream_t)stream, a, states, n, (int)chunk, bits);
+    // each tile's states go to as many workgroups as fill the card, of a few
+    // states a wave
+    const int64_t tiles = (vocab->V + kTile - 1) / kTile, places = kEntries > 8192 ? 256 : 512;
+    int64_t parts = places > tiles ? places / tiles : 1;
+    const int64_t most = (n + kWaves - 1) / kWaves;
+    parts = parts < most ? parts : most;
+    const int64_t part = (n + parts - 1) / parts;
+    hipLaunchKernelGGL(k_masks<kEntries>, dim3((unsigned)tiles, (unsigned)((n + part - 1) / part)),
+                       dim3(kThreads), 0, (hipStream_t)stream, a, states, n, (int)part, bits);
   });
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_DEVICE;
 }
