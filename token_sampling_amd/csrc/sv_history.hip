@@ -5,6 +5,7 @@
 namespace sv {
 namespace {
 
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr int kGridZ = 32768;  // sessions of a launch
 // Up to so many tokens a session, k_count_few: prompts of 400 tokens take 2.7
@@ -50,7 +51,7 @@ __device__ inline void clear_row(uint32_t* row, int n, int at, int step) {
   const int head = (int)((16 - (uintptr_t)row % 16) % 16 / 4);
   const int body = n > head ? (n - head) / 4 : 0;
   if (at < head && at < n) row[at] = 0;
-  for (int i = at; i < body; i += step) *(uint4*)(row + head + 4 * i) = uint4{0, 0, 0, 0};
+  for (int i = at; i < body; i += step) *(u32x4*)(row + head + 4 * i) = u32x4{0, 0, 0, 0};
   for (int i = head + 4 * body + at; i < n; i += step) row[i] = 0;
 }
 __global__ __launch_bounds__(kThreads) void k_clear(CountArgs a) {
@@ -106,14 +107,15 @@ __global__ __launch_bounds__(kManyThreads) void k_count_many(CountArgs a) {
   __syncthreads();
   for (; lo < hi; lo += (int64_t)gridDim.x * kPart) {
     const int n = hi - lo < kPart ? (int)(hi - lo) : kPart;
+    int32_t t[kPart / kManyThreads];
+#pragma unroll
+    for (int k = 0; k < kPart / kManyThreads; ++k)
+      t[k] = a.tokens[lo + min(k * kManyThreads + (int)threadIdx.x, n - 1)];
 #pragma unroll
     for (int k = 0; k < kPart / kManyThreads; ++k) {
-      const int i = k * kManyThreads + threadIdx.x;
-      if (i >= n) break;
-      const int64_t t = (int64_t)a.tokens[lo + i] - v0;
-      if (t < 0 || t >= ids) continue;
-      if (kPlane) atomicAdd(lds + t, 1u);
-      else atomicOr(lds + t / 32, 1u << (t % 32));
+      if (k * kManyThreads + (int)threadIdx.x >= n || t[k] < v0 || t[k] - v0 >= ids) continue;
+      if (kPlane) atomicAdd(lds + (t[k] - v0), 1u);
+      else atomicOr(lds + (t[k] - v0) / 32, 1u << (t[k] % 32));
     }
   }
   __syncthreads();
@@ -133,9 +135,11 @@ __global__ __launch_bounds__(kManyThreads) void k_count_many(CountArgs a) {
 }
 
 template <int kPlane>
-void launch_many(CountArgs a, int64_t most, hipStream_t st) {
+void launch_many(CountArgs a, int64_t mean, hipStream_t st) {
   constexpr int kRange = kPlane ? 1 << 14 : 1 << 18;
-  const int64_t parts = (most + kPart - 1) / kPart;
+  // workgroups for a session of the mean length, twice as many where lengths
+  // are not known here; longer ones take more turns
+  const int64_t parts = (mean * (a.offsets ? 2 : 1) + kPart - 1) / kPart;
   for (a.b0 = 0; a.b0 < a.B; a.b0 += kGridZ) {
     const dim3 grid((unsigned)(parts < 16 ? parts : 16), (a.V + kRange - 1) / kRange,
                     a.B - a.b0 < kGridZ ? a.B - a.b0 : kGridZ);
@@ -169,8 +173,8 @@ extern "C" int sv_count_tokens(const sv_history* history, const int32_t* slots,
   // tokens of a session: L, or on average in a line
   const int64_t mean = offsets ? ((int64_t)L + B - 1) / B : L;
   if (mean > (plane ? kFewOutput : kFewPrompt)) {
-    if (plane) launch_many<1>(a, L, st);
-    else launch_many<0>(a, L, st);
+    if (plane) launch_many<1>(a, mean, st);
+    else launch_many<0>(a, mean, st);
   } else if (L > 0) {
     const unsigned gx = (unsigned)((mean + kThreads - 1) / kThreads);
     hipLaunchKernelGGL(k_count_few, dim3(gx, gy), dim3(kThreads), 0, st, a);
