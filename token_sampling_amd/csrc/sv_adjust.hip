@@ -10,6 +10,8 @@
 #include <limits.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "sv_common.hpp"
 
 namespace sv {
@@ -18,6 +20,7 @@ namespace {
 constexpr int64_t kWantedWaves = 8192;  // two for each place of a wave in the card's SIMDs
 constexpr int kGridY = 32768;           // sessions of a launch
 constexpr int kBatch = 4;               // logits of a lane in flight, in place
+constexpr int kTurns = 4;               // turns over a tile's listed tokens whose reads overlap
 
 struct AdjustArgs {
   const void* logits;
@@ -158,6 +161,11 @@ __device__ inline float from_bits(uint32_t x, float) { return __builtin_bit_cast
 template <typename T>
 constexpr uint32_t kMinusInf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
 
+// What a token's logit gets added: its bias, less its penalties at count c.
+__device__ inline float term_of(const Session& s, float bias, int c) {
+  return c > 0 ? bias - fmaf(s.frequency, (float)c, s.presence) : bias;
+}
+
 // A touched token of a tile, 16 bits: its place in the tile and
 constexpr uint32_t kPlace = 0x0FFF;
 constexpr uint32_t kRep = 0x1000;   // seen: the repetition penalty applies
@@ -193,7 +201,7 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
   constexpr uint32_t kFull = G * E == 32 ? ~0u : (1u << (G * E)) - 1;
   static_assert(G * E <= 32 && kTile <= (int)kPlace + 1, "a lane's tokens fit one word");
   constexpr bool kVectors = !kInPlace || kMasks;  // whole vectors move
-  __shared__ __attribute__((aligned(16))) T raw[kVectors ? kTile : 1];
+  __shared__ __attribute__((aligned(16))) T raw[kTile];
   __shared__ float term[kTile];
   __shared__ uint16_t list[kTile];
   __shared__ uint32_t bits[kTile / 32];
@@ -325,11 +333,24 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     wave_sync();
     any |= noted();
   }
+  // those before the first row count from the start: 16 bits a token, in raw
+  const uint64_t early = r0 < kWave ? mine & ~(~0ull << r0) : mine;
+  typedef uint16_t u16_alias __attribute__((may_alias));
+  typedef uint32_t u32_alias __attribute__((may_alias));
+  const u16_alias* early_count = (const u16_alias*)raw;
+  if (early != 0) {
+    for (int w = lane; w < kTile / 2; w += kWave) ((u32_alias*)raw)[w] = 0;
+    wave_sync();
+    if ((early >> lane) & 1)
+      atomicAdd((u32_alias*)raw + (s.token - v0) / 2, 1u << (16 * ((s.token - v0) % 2)));
+    wave_sync();
+  }
   const int count = __popc(any);
   const int upto = wave_incl_scan(count);
   const int listed = lane_read(upto, kWave - 1);
+  const int base = upto - count;  // the list has a lane's tokens from here on, in order
   if (listed > 0) {
-    int at = upto - count;
+    int at = base;
     for (uint32_t w = any; w != 0; w &= w - 1) {
       const int k = __builtin_ctz(w);
       const uint32_t bit = 1u << k;
@@ -341,14 +362,19 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     }
     wave_sync();
     for (int j = lane; j < listed; j += kWave) {
-      const uint32_t e = list[j];
+      uint32_t e = list[j];
       const int i = e & kPlace;
       float t = e & kBias ? term[i] : 0.f;
-      if (e & kHad) {
-        const int c = a.counts[(size_t)s.slot * a.V + v0 + i];
-        if (c > 0) t -= s.frequency * (float)c + s.presence;
+      int c = e & kHad ? a.counts[(size_t)s.slot * a.V + v0 + i] : 0;
+      if (early != 0) {
+        const int more = early_count[i];
+        c += more;
+        if (more > 0) {
+          e |= kRep | kHad | kOn;
+          list[j] = (uint16_t)e;
+        }
       }
-      term[i] = t;
+      term[i] = term_of(s, t, c);
     }
     wave_sync();
   }
@@ -361,18 +387,24 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     return (e & kRep ? z * f : z) + t;
   };
   auto meet = [&](int d) {  // drafted token d counts from here on
-    const int place = lane_read(s.token, d) - v0;
-    for (int j = lane; j < listed; j += kWave) {
-      const uint32_t e = list[j];
-      if ((int)(e & kPlace) == place) {
-        term[place] -= e & kHad ? s.frequency : s.frequency + s.presence;
-        list[j] = (uint16_t)(e | kRep | kHad | kOn);
-      }
-    }
+    const int v = lane_read(s.token, d), place = v - v0;
+    const int owner = place % L::kGroup / E, k = place / L::kGroup * E + place % E;
+    const int j = lane_read(base, owner) + __popc(lane_read(any, owner) & ((1u << k) - 1));
+    // the term anew from the count, so that a row's result does not depend on
+    // the row its wave began with
+    int c = __popcll(__ballot(s.token == v && lane <= d));
+    if ((lane_read(had, owner) >> k) & 1) c += a.counts[(size_t)s.slot * a.V + v];
+    float t = 0.f;
+    const uint32_t e = list[j];
+    if (e & kBias)
+      for (int i = bias_lo + lane; i < bias_hi; i += kWave)
+        if (a.bias_id[i] == v) t = a.bias_val[i];
+    t = wave_reduce(t, OpAdd());
+    wave_sync();
+    term[place] = term_of(s, t, c);  // every lane the same
+    list[j] = (uint16_t)(e | kRep | kHad | kOn);
     wave_sync();
   };
-  for (int d = 0; d < r0; ++d)
-    if ((mine >> d) & 1) meet(d);
 
   for (int r = r0; r < r1;) {
     if (r > r0 && ((mine >> (r - 1)) & 1)) meet(r - 1);
@@ -423,11 +455,28 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
         for (int g = 0; g < G; ++g)
           if ((any >> (g * E)) & kAll) *(u32x4*)(raw + g * L::kGroup + first) = y[g];
         wave_sync();
-        for (int j = lane; j < listed; j += kWave) {
-          const uint32_t e = list[j];
-          const int i = e & kPlace;
-          if (e & kOn) raw[i] = (T)changed((float)raw[i], e, term[i]);
-        }
+        auto turn = [&](int j0, auto turns) {  // whose reads go out together
+          constexpr int N = decltype(turns)::value;
+          uint32_t e[N];
+          float t[N], z[N];
+#pragma unroll
+          for (int q = 0; q < N; ++q) {
+            const int j = j0 + q * kWave + lane;
+            e[q] = j < listed ? list[j] : 0;
+          }
+#pragma unroll
+          for (int q = 0; q < N; ++q) {
+            t[q] = term[e[q] & kPlace];
+            z[q] = (float)raw[e[q] & kPlace];
+          }
+#pragma unroll
+          for (int q = 0; q < N; ++q)
+            if (e[q] & kOn) raw[e[q] & kPlace] = (T)changed(z[q], e[q], t[q]);
+        };
+        int j0 = 0;
+        for (; listed - j0 > kWave; j0 += kTurns * kWave)
+          turn(j0, std::integral_constant<int, kTurns>());
+        if (j0 < listed) turn(j0, std::integral_constant<int, 1>());
         wave_sync();
 #pragma unroll
         for (int g = 0; g < G; ++g)
@@ -466,8 +515,10 @@ template <typename T, int kSize, bool kInPlace, bool kMasks>
 void launch(AdjustArgs a, hipStream_t st) {
   constexpr int G = kSize * (int)sizeof(T) / 2, kTile = G * Lanes<T>::kGroup;
   const int64_t tiles = (a.V + kTile - 1) / kTile;
-  // rows go to several waves where a wave per tile would leave the card idle
-  int64_t chunks = (kWantedWaves + tiles * a.B - 1) / (tiles * a.B);
+  // rows go to several waves where a wave per tile would leave the card idle; a
+  // quarter as many where rows move their listed tokens alone
+  const int64_t wanted = kInPlace && !kMasks ? kWantedWaves / 4 : kWantedWaves;
+  int64_t chunks = (wanted + tiles * a.B - 1) / (tiles * a.B);
   chunks = chunks < a.R ? chunks : a.R;
   a.chunk = (int)((a.R + chunks - 1) / chunks);
   chunks = (a.R + a.chunk - 1) / a.chunk;
