@@ -137,6 +137,23 @@ def test_dense_rules(dtype):
     both_ways(Case(3, 3, 6, 7, 3001, dtype, hist=40000, n_bias=3001))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("V", [110001, 110008])
+def test_many_rows(V, dtype):
+    """Enough rows for a wave a tile, at odd addresses and at even ones."""
+    both_ways(Case(5, 40, 2, 3, V, dtype, hist=2000, n_bias=200))
+
+
+@pytest.mark.parametrize("rules", ["p", "pb", "pbm"])
+@pytest.mark.parametrize("B", [1, 40, 400])
+def test_drafted_tokens_over_and_over(B, rules):
+    """Every draft one of three tokens, biased and counted: met in each row, or
+    before the first row of a wave."""
+    case = Case(6, B, 20, 21, 1100, "fp32", rules=rules, n_bias=700)
+    case.tokens = np.random.default_rng(1).choice([3, 600, 1099], case.tokens.shape).astype(np.int32)
+    both_ways(case)
+
+
 def test_no_history():
     """Penalties without a history count the drafted tokens alone."""
     case = Case(8, 4, 9, 10, 500, "fp32", rules="p", ragged=False)

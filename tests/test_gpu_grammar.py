@@ -57,6 +57,25 @@ def test_numbers_of_states(n):
     check_masks(nxt, accept, tokens, [], rng.integers(-1, 12, n).tolist())
 
 
+@pytest.mark.parametrize("S,C", [(30, 11), (600, 90), (700, 256), (250, 256), (1500, 37)])
+@pytest.mark.parametrize("V,n", [(77, 9000), (2500, 5000), (6200, 40)])
+def test_tables_by_units(S, C, V, n):
+    """Automata of every place (both sizes in LDS, global memory), with a few
+    states a tile and with many."""
+    rng = np.random.default_rng(S + V)
+    nxt, accept = ref.random_grammar(rng, S, C, live=0.9)
+    tokens = ref.random_vocab(rng, V, longest=20)
+    used = rng.integers(0, S, 25)  # the reference walks each state once
+    check_masks(nxt, accept, tokens, [7, 70], np.concatenate([[-1, S], rng.choice(used, n)]).tolist())
+
+
+def test_more_states_than_a_workgroup_has_at_hand():
+    rng = np.random.default_rng(9)
+    nxt, accept = ref.random_grammar(rng, 10, 6, live=0.8)
+    tokens = ref.random_vocab(rng, 70001, longest=3, control=40)
+    check_masks(nxt, accept, tokens, [0, 70000], rng.integers(-1, 10, 9000).tolist())
+
+
 def test_long_tokens():
     """Tokens much longer than a word, refused at their first and at their last byte."""
     nxt = np.full((3, 256), -1, np.int32)

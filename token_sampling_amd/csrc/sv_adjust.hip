@@ -22,6 +22,8 @@ constexpr int kGridY = 32768;           // sessions of a launch
 constexpr int kBatch = 4;               // logits of a lane in flight, in place
 constexpr int kTurns = 4;               // turns over a tile's listed tokens whose reads overlap
 
+__device__ uint32_t nothing[4];  // where a vector that is not needed comes from
+
 struct AdjustArgs {
   const void* logits;
   int64_t in_session, in_row;
@@ -278,6 +280,37 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     }
   };
 
+  // The same for a tile that the row has all of, rows past the last included:
+  // vectors that are not needed come from nothing, so that every lane loads.
+  [[maybe_unused]] auto load_whole = [&](int r, uint32_t mk, u32x4 (&x)[G]) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const bool wanted = r < r1 && ((mk >> (g * E)) & kAll) != 0;
+      x[g] = load16(wanted ? in + r * a.in_row + g * L::kGroup + first : (const T*)nothing);
+    }
+  };
+  // A row's mask bytes on the way.
+  struct Ahead {
+    bool masked;
+    Bytes bytes;
+  };
+  [[maybe_unused]] auto mask_ahead = [&](int r) {
+    Ahead h = {};
+    if constexpr (kMasks) {
+      const int k = mask_row(r);
+      h.masked = k >= 0;
+      const uint8_t* row = h.masked ? (const uint8_t*)(a.mask_bits + (size_t)k * a.W) + v0 / 8
+                                    : (const uint8_t*)nothing;
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const int i = g * L::kGroup + first;
+        h.bytes.of[g] = row[h.masked && i < left ? i / 8 : 0];
+      }
+    }
+    return h;
+  };
+  [[maybe_unused]] auto ahead_of = [&](const Ahead& h) { return h.masked ? packed(h.bytes) : kFull; };
+
   // ---- what the rows share; loads first
   Bytes prompt = {}, output = {}, mask = {};
   if (s.slot >= 0) {
@@ -296,8 +329,13 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     bias = a.bias_val[bias_lo + lane];
   }
   u32x4 x[G];
+  [[maybe_unused]] Ahead ahead = {};
+  if constexpr (!kInPlace) ahead = mask_ahead(r0 + 1);
   uint32_t mk = mask0 < 0 ? kFull : packed(mask);
-  if constexpr (!kInPlace) load(r0, mk, kFull, x);
+  if constexpr (!kInPlace) {
+    if (left >= kTile) load_whole(r0, mk, x);
+    else load(r0, mk, kFull, x);
+  }
 
   const uint32_t had = packed(output), rep = packed(prompt) | had;
   // drafted tokens of this tile that rows before r1 meet
@@ -406,6 +444,90 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     wave_sync();
   };
 
+  // Row r from its vectors y: the listed tokens, the mask, and out it goes.  kWhole:
+  // the row has all of the tile's tokens.
+  auto finish = [&](int r, uint32_t mk, u32x4 (&y)[G], auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+    if (listed > 0) {
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if ((any >> (g * E)) & kAll) *(u32x4*)(raw + g * L::kGroup + first) = y[g];
+      wave_sync();
+      auto turn = [&](int j0, auto turns) {  // whose reads go out together
+        constexpr int N = decltype(turns)::value;
+        uint32_t e[N];
+        float t[N], z[N];
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          const int j = j0 + q * kWave + lane;
+          e[q] = j < listed ? list[j] : 0;
+        }
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          t[q] = term[e[q] & kPlace];
+          z[q] = (float)raw[e[q] & kPlace];
+        }
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          if (e[q] & kOn) raw[e[q] & kPlace] = (T)changed(z[q], e[q], t[q]);
+      };
+      int j0 = 0;
+      for (; listed - j0 > kWave; j0 += kTurns * kWave)
+        turn(j0, std::integral_constant<int, kTurns>());
+      if (j0 < listed) turn(j0, std::integral_constant<int, 1>());
+      wave_sync();
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+        if ((any >> (g * E)) & kAll) y[g] = *(const u32x4*)(raw + g * L::kGroup + first);
+    }
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int i = g * L::kGroup + first;
+      const uint32_t ok = (mk >> (g * E)) & kAll;
+      if ((!kWhole && i >= left) || (kInPlace && ((any >> (g * E)) & kAll) == 0 && ok == kAll)) continue;
+      if (ok != kAll) {
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const uint32_t sel = select_word(ok, d, T(0)), w = y[g][d];
+          y[g][d] = (w & sel) | (kMinusInf<T> & ~sel);
+        }
+      }
+      T* p = out + r * a.out_row + i;
+      if (kWhole || i + E <= left) {
+        store16(p, y[g]);
+      } else {
+        T t[E];
+        __builtin_memcpy(t, &y[g], 16);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+          if (i + k < left) p[k] = t[k];
+      }
+    }
+  };
+
+  if constexpr (!kInPlace) {
+    if (left >= kTile) {
+      // two rows in turn, the next one's loads on the way while one is worked on;
+      // no load or store is passed over, so that each wait is for its own
+      __builtin_amdgcn_s_waitcnt(0);
+      auto half = [&](int r, u32x4 (&x0)[G], uint32_t m0, u32x4 (&x1)[G], uint32_t& m1) {
+        if (r > r0 && ((mine >> (r - 1)) & 1)) meet(r - 1);
+        m1 = ahead_of(ahead);
+        ahead = mask_ahead(r + 2);
+        load_whole(r + 1, m1, x1);
+        finish(r, m0, x0, std::true_type());
+      };
+      u32x4 x1[G];
+      uint32_t m1;
+      for (int r = r0;;) {
+        half(r, x, mk, x1, m1);
+        if (++r >= r1) break;
+        half(r, x1, m1, x, mk);
+        if (++r >= r1) break;
+      }
+      return;
+    }
+  }
   for (int r = r0; r < r1;) {
     if (r > r0 && ((mine >> (r - 1)) & 1)) meet(r - 1);
     if (!kVectors || (kInPlace && mask_row(r) < 0)) {
@@ -450,61 +572,7 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
       if constexpr (!kInPlace) {
         if (r + 1 < r1) load(r + 1, next, kFull, x);
       }
-      if (listed > 0) {
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-          if ((any >> (g * E)) & kAll) *(u32x4*)(raw + g * L::kGroup + first) = y[g];
-        wave_sync();
-        auto turn = [&](int j0, auto turns) {  // whose reads go out together
-          constexpr int N = decltype(turns)::value;
-          uint32_t e[N];
-          float t[N], z[N];
-#pragma unroll
-          for (int q = 0; q < N; ++q) {
-            const int j = j0 + q * kWave + lane;
-            e[q] = j < listed ? list[j] : 0;
-          }
-#pragma unroll
-          for (int q = 0; q < N; ++q) {
-            t[q] = term[e[q] & kPlace];
-            z[q] = (float)raw[e[q] & kPlace];
-          }
-#pragma unroll
-          for (int q = 0; q < N; ++q)
-            if (e[q] & kOn) raw[e[q] & kPlace] = (T)changed(z[q], e[q], t[q]);
-        };
-        int j0 = 0;
-        for (; listed - j0 > kWave; j0 += kTurns * kWave)
-          turn(j0, std::integral_constant<int, kTurns>());
-        if (j0 < listed) turn(j0, std::integral_constant<int, 1>());
-        wave_sync();
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-          if ((any >> (g * E)) & kAll) y[g] = *(const u32x4*)(raw + g * L::kGroup + first);
-      }
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const int i = g * L::kGroup + first;
-        const uint32_t ok = (mk >> (g * E)) & kAll;
-        if (i >= left || (kInPlace && ((any >> (g * E)) & kAll) == 0 && ok == kAll)) continue;
-        if (ok != kAll) {
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const uint32_t sel = select_word(ok, d, T(0)), w = y[g][d];
-            y[g][d] = (w & sel) | (kMinusInf<T> & ~sel);
-          }
-        }
-        T* p = out + r * a.out_row + i;
-        if (i + E <= left) {
-          store16(p, y[g]);
-        } else {
-          T t[E];
-          __builtin_memcpy(t, &y[g], 16);
-#pragma unroll
-          for (int k = 0; k < E; ++k)
-            if (i + k < left) p[k] = t[k];
-        }
-      }
+      finish(r, mk, y, std::false_type());
       mk = next;
       ++r;
     }
