@@ -154,6 +154,10 @@ def test_drafted_tokens_over_and_over(B, rules):
     both_ways(case)
 
 
+def test_more_sessions_than_a_launch():
+    both_ways(Case(7, 33000, 1, 2, 9, "bf16", hist=5))
+
+
 def test_no_history():
     """Penalties without a history count the drafted tokens alone."""
     case = Case(8, 4, 9, 10, 500, "fp32", rules="p", ragged=False)

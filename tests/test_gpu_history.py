@@ -52,6 +52,24 @@ def test_rows_of_tokens(B, L, V, prompt, clear):
         same(h, counts, seen)
 
 
+@pytest.mark.parametrize("L", [2, 2100])
+def test_more_sessions_than_a_launch(L):
+    rng = np.random.default_rng(2)
+    B, V = 33000, 5
+    h = sv.make_history(B, V)
+    tokens = rng.integers(-1, V, (B, L)).astype(np.int32)
+    sv.count_tokens(h, dev(tokens))
+    torch.cuda.synchronize()
+    want = np.stack([(tokens == v).sum(1) for v in range(V)], 1)
+    assert np.array_equal(h.counts.cpu().numpy(), want)
+    assert np.array_equal(ref.unpack(h.seen[:, 1].cpu().numpy(), V), want > 0)
+    assert not h.seen[:, 0].any()
+    sv.count_tokens(h, dev(tokens), prompt=True, clear=True)
+    torch.cuda.synchronize()
+    assert not h.counts.any() and not h.seen[:, 1].any()
+    assert np.array_equal(ref.unpack(h.seen[:, 0].cpu().numpy(), V), want > 0)
+
+
 @pytest.mark.parametrize("prompt", [True, False])
 @pytest.mark.parametrize("lens", [[0], [1], [3, 0, 5], [0, 0, 0], [700, 1, 0, 12000], [40000]])
 def test_line_of_tokens(lens, prompt):

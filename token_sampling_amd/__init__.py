@@ -684,14 +684,16 @@ def _launch(dev, stream):
 
 
 def _want(t, name, dtype, shape, device):
-    """_check, quick where t is as it should be: these calls are short enough on
-    the GPU for the host's checks to count."""
+    """t's address, after _check's checks, quick where t is as it should be: these
+    calls are short enough on the GPU for the host's checks to count."""
     try:
-        if (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
-            return
+        if (t.dtype is dtype and t.get_device() == device.index and t.shape == shape
+                and t.is_contiguous()):
+            return t.data_ptr()
     except AttributeError:
         pass
     _check(t, name, dtype, shape, device)
+    return t.data_ptr()
 
 
 def _device_of(t, name):
@@ -704,17 +706,18 @@ def _device_of(t, name):
     return t.device
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _int32(n, name):
+    if n >= 1 << 31:
+        raise ValueError(f"{name} holds 2^31 entries or more")
+    return n
 
 
 def _history_struct(history, V, dev):
     import torch
 
     n = history.counts.shape[0]
-    _want(history.counts, "history.counts", torch.int32, (n, V), dev)
-    _want(history.seen, "history.seen", torch.int32, (n, 2, (V + 31) // 32), dev)
-    return _History(history.counts.data_ptr(), history.seen.data_ptr(), n)
+    return _History(_want(history.counts, "history.counts", torch.int32, (n, V), dev),
+                    _want(history.seen, "history.seen", torch.int32, (n, 2, (V + 31) // 32), dev), n)
 
 
 def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slots=None, bias=None,
@@ -750,6 +753,7 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
     sb, sr, sv_ = logits.stride()
     if V > 1 and sv_ != 1:
         raise ValueError("the logits of a row must be contiguous")
+    p_tokens = p_m = p_pen = p_slots = hist = bs = mk = None
     if tokens is None:
         if R != 1:
             raise ValueError("tokens may be left out only for one row a session")
@@ -758,34 +762,30 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
             raise ValueError("m needs tokens")
     else:
         M = R - 1 if tokens.dim() == 2 and tokens.shape[1] == R - 1 else R
-        _want(tokens, "tokens", torch.int32, (B, M), dev)
+        p_tokens = _want(tokens, "tokens", torch.int32, (B, M), dev)
         if m is not None:
-            _want(m, "m", torch.int32, (B,), dev)
+            p_m = _want(m, "m", torch.int32, (B,), dev)
     if penalties is not None:
-        _want(penalties, "penalties", torch.uint8, (B, 16), dev)
-    hist = bs = mk = None
+        p_pen = _want(penalties, "penalties", torch.uint8, (B, 16), dev)
     if history is not None:
         hist = ctypes.byref(_history_struct(history, V, dev))
         if slots is None and history.counts.shape[0] < B:
             raise ValueError("history has fewer slots than sessions")
     if slots is not None:
-        _want(slots, "slots", torch.int32, (B,), dev)
+        p_slots = _want(slots, "slots", torch.int32, (B,), dev)
     if bias is not None:
-        n = bias.ids.numel()
-        _want(bias.offsets, "bias.offsets", torch.int32, (B + 1,), dev)
-        _want(bias.ids, "bias.ids", torch.int32, (n,), dev)
-        _want(bias.values, "bias.values", torch.float32, (n,), dev)
-        bs = ctypes.byref(_Bias(bias.offsets.data_ptr(), bias.ids.data_ptr(),
-                                bias.values.data_ptr(), n))
+        n = _int32(bias.ids.numel(), "bias")
+        bs = ctypes.byref(_Bias(_want(bias.offsets, "bias.offsets", torch.int32, (B + 1,), dev),
+                                _want(bias.ids, "bias.ids", torch.int32, (n,), dev),
+                                _want(bias.values, "bias.values", torch.float32, (n,), dev), n))
     if (masks is None) != (mask_rows is None):
         raise ValueError("masks and mask_rows go together")
     if masks is not None:
         n = masks.shape[0]
-        _want(masks, "masks", torch.int32, (n, (V + 31) // 32), dev)
-        _want(mask_rows, "mask_rows", torch.int32, (B, R), dev)
         if n < 1:
             raise ValueError("masks must hold a row")
-        mk = ctypes.byref(_Masks(masks.data_ptr(), mask_rows.data_ptr(), n))
+        mk = ctypes.byref(_Masks(_want(masks, "masks", torch.int32, (n, (V + 31) // 32), dev),
+                                 _want(mask_rows, "mask_rows", torch.int32, (B, R), dev), n))
     handle, on = _launch(dev, stream)
     with on:
         if out is None:
@@ -806,9 +806,9 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
             status = torch.empty(B, dtype=torch.int32, device=dev)
         else:
             _want(status, "status", torch.int32, (B,), dev)
-        rc = lib().sv_adjust_logits(logits.data_ptr(), sb, sr, dt, _ptr(tokens), _ptr(m),
-                                    _ptr(penalties), hist, _ptr(slots), bs, mk, B, M, R, V,
-                                    out.data_ptr(), status.data_ptr(), handle)
+        rc = lib().sv_adjust_logits(logits.data_ptr(), sb, sr, dt, p_tokens, p_m, p_pen, hist,
+                                    p_slots, bs, mk, B, M, R, V, out.data_ptr(),
+                                    status.data_ptr(), handle)
     if rc != OK:
         raise SvError(f"sv_adjust_logits failed: {strerror(rc)} ({rc})")
     return {"logits": out, "status": status}
@@ -835,27 +835,28 @@ def count_tokens(history, tokens, slots=None, lens=None, offsets=None, prompt=Fa
     dev = _device_of(tokens, "tokens")
     V = history.counts.shape[-1]
     hist = _history_struct(history, V, dev)
+    p_offsets = p_lens = p_slots = None
     if offsets is not None:
         if lens is not None:
             raise ValueError("give lens or offsets, not both")
-        B, L = offsets.numel() - 1, tokens.numel()
-        _want(tokens, "tokens", torch.int32, (L,), dev)
-        _want(offsets, "offsets", torch.int32, (B + 1,), dev)
+        B, L = offsets.numel() - 1, _int32(tokens.numel(), "tokens")
+        p_tokens = _want(tokens, "tokens", torch.int32, (L,), dev)
+        p_offsets = _want(offsets, "offsets", torch.int32, (B + 1,), dev)
     else:
         if tokens.dim() != 2:
             raise ValueError("tokens must be [B, L] (or one line, with offsets)")
         B, L = tokens.shape
-        _want(tokens, "tokens", torch.int32, tokens.shape, dev)
+        p_tokens = _want(tokens, "tokens", torch.int32, tokens.shape, dev)
         if lens is not None:
-            _want(lens, "lens", torch.int32, (B,), dev)
+            p_lens = _want(lens, "lens", torch.int32, (B,), dev)
     if slots is not None:
-        _want(slots, "slots", torch.int32, (B,), dev)
+        p_slots = _want(slots, "slots", torch.int32, (B,), dev)
     elif history.counts.shape[0] < B:
         raise ValueError("history has fewer slots than sessions")
     handle, on = _launch(dev, stream)
     with on:
-        rc = lib().sv_count_tokens(ctypes.byref(hist), _ptr(slots), tokens.data_ptr(), _ptr(offsets),
-                                   _ptr(lens), B, L, V, 0 if prompt else 1, int(clear), handle)
+        rc = lib().sv_count_tokens(ctypes.byref(hist), p_slots, p_tokens, p_offsets, p_lens, B, L, V,
+                                   0 if prompt else 1, int(clear), handle)
     if rc != OK:
         raise SvError(f"sv_count_tokens failed: {strerror(rc)} ({rc})")
 
@@ -865,15 +866,13 @@ def _grammar_structs(grammar, vocab, dev):
 
     S, C = grammar.next.shape
     V = vocab.offsets.numel() - 1
-    _want(grammar.next, "grammar.next", torch.int32, (S, C), dev)
-    _want(grammar.classes, "grammar.classes", torch.uint8, (256,), dev)
-    _want(grammar.accept, "grammar.accept", torch.uint8, (S,), dev)
-    _want(vocab.bytes, "vocab.bytes", torch.uint8, (vocab.bytes.numel(),), dev)
-    _want(vocab.offsets, "vocab.offsets", torch.int32, (V + 1,), dev)
-    _want(vocab.end, "vocab.end", torch.int32, (vocab.end.numel(),), dev)
-    g = _Grammar(grammar.next.data_ptr(), grammar.classes.data_ptr(), grammar.accept.data_ptr(), S, C)
-    v = _Vocab(vocab.bytes.data_ptr(), vocab.offsets.data_ptr(), vocab.end.data_ptr(),
-               vocab.bytes.numel(), vocab.end.numel(), V)
+    n, ends = _int32(vocab.bytes.numel(), "vocab.bytes"), vocab.end.numel()
+    g = _Grammar(_want(grammar.next, "grammar.next", torch.int32, (S, C), dev),
+                 _want(grammar.classes, "grammar.classes", torch.uint8, (256,), dev),
+                 _want(grammar.accept, "grammar.accept", torch.uint8, (S,), dev), S, C)
+    v = _Vocab(_want(vocab.bytes, "vocab.bytes", torch.uint8, (n,), dev),
+               _want(vocab.offsets, "vocab.offsets", torch.int32, (V + 1,), dev),
+               _want(vocab.end, "vocab.end", torch.int32, (ends,), dev), n, ends, V)
     return ctypes.byref(g), ctypes.byref(v), V
 
 
@@ -884,15 +883,15 @@ def grammar_masks(grammar, vocab, states, out=None, stream=None):
 
     dev = _device_of(states, "states")
     g, v, V = _grammar_structs(grammar, vocab, dev)
-    n = states.numel()
-    _want(states, "states", torch.int32, (n,), dev)
+    n = _int32(states.numel(), "states")
+    p_states = _want(states, "states", torch.int32, (n,), dev)
     handle, on = _launch(dev, stream)
     with on:
         if out is None:
             out = torch.empty((n, (V + 31) // 32), dtype=torch.int32, device=dev)
         else:
             _want(out, "out", torch.int32, (n, (V + 31) // 32), dev)
-        rc = lib().sv_grammar_masks(g, v, states.data_ptr(), n, out.data_ptr(), handle)
+        rc = lib().sv_grammar_masks(g, v, p_states, n, out.data_ptr(), handle)
     if rc != OK:
         raise SvError(f"sv_grammar_masks failed: {strerror(rc)} ({rc})")
     return out
@@ -911,10 +910,9 @@ def grammar_advance(grammar, vocab, states, tokens, lens=None, out=None, stream=
     if tokens.dim() != 2:
         raise ValueError("tokens must be [B, L]")
     B, L = tokens.shape
-    _want(tokens, "tokens", torch.int32, tokens.shape, dev)
-    _want(states, "states", torch.int32, (B,), dev)
-    if lens is not None:
-        _want(lens, "lens", torch.int32, (B,), dev)
+    p_tokens = _want(tokens, "tokens", torch.int32, tokens.shape, dev)
+    p_states = _want(states, "states", torch.int32, (B,), dev)
+    p_lens = None if lens is None else _want(lens, "lens", torch.int32, (B,), dev)
     handle, on = _launch(dev, stream)
     with on:
         if out is None:
@@ -923,7 +921,7 @@ def grammar_advance(grammar, vocab, states, tokens, lens=None, out=None, stream=
         else:
             _want(out["states"], "out['states']", torch.int32, (B, L + 1), dev)
             _want(out["last"], "out['last']", torch.int32, (B,), dev)
-        rc = lib().sv_grammar_advance(g, v, states.data_ptr(), tokens.data_ptr(), _ptr(lens), B, L,
+        rc = lib().sv_grammar_advance(g, v, p_states, p_tokens, p_lens, B, L,
                                       out["states"].data_ptr(), out["last"].data_ptr(), handle)
     if rc != OK:
         raise SvError(f"sv_grammar_advance failed: {strerror(rc)} ({rc})")
