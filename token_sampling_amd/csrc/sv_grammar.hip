@@ -201,13 +201,31 @@ __global__ __launch_bounds__(kThreads) void k_masks(GrammarArgs a, const int32_t
   __shared__ int32_t from_state[kStates];  // states in work, -1 where every token is allowed
   __shared__ bool accepts[kStates];
   __shared__ int next;  // the first that no wave has taken
-  const Table<kEntries, true> table(a.g, lds);
-  columns_of(a.g, column);
   const int lane = __lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int W = (a.v.V + 31) / 32, tile = blockIdx.x;
   int k0 = blockIdx.y * part;
   const int k1 = n - k0 < part ? n : k0 + part;
+  // the tokens' loads go ahead of the table's
+  int len[kEach];
+  uint8_t held[kEach][kHeld];
+  {
+    int lo[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int id = min(tile * kTile + e * kThreads + (int)threadIdx.x, a.v.V - 1);
+      lo[e] = offset_of(a.v, id);
+      len[e] = offset_of(a.v, id + 1);
+    }
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      len[e] -= lo[e];
+      if (tile * kTile + e * kThreads + (int)threadIdx.x >= a.v.V) len[e] = 0;
+      if (len[e] > 0) held_bytes(a.v, lo[e], len[e], held[e]);
+    }
+  }
+  const Table<kEntries, true> table(a.g, lds);
+  columns_of(a.g, column);
   for (int i = threadIdx.x; i < kParts * (kNone + 1); i += kThreads) (&begins[0][0])[i] = 0;
   if (threadIdx.x < kWords) ends[threadIdx.x] = 0;
   __syncthreads();
@@ -219,23 +237,8 @@ __global__ __launch_bounds__(kThreads) void k_masks(GrammarArgs a, const int32_t
       const int i = a.v.end[threadIdx.x] - tile * kTile;
       if (i >= 0 && i < kTile && i + tile * kTile < a.v.V) atomicOr(ends + i / 32, 1u << (i % 32));
     }
-    int lo[kEach], len[kEach], first[kEach];
-    uint8_t held[kEach][kHeld];
+    int first[kEach];
     uint32_t rank[kEach];
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int id = min(tile * kTile + e * kThreads + (int)threadIdx.x, a.v.V - 1);
-      lo[e] = offset_of(a.v, id);
-      len[e] = offset_of(a.v, id + 1);
-    }
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      len[e] -= lo[e];
-      if (tile * kTile + e * kThreads + (int)threadIdx.x >= a.v.V) len[e] = 0;
-    }
-#pragma unroll
-    for (int e = 0; e < kEach; ++e)
-      if (len[e] > 0) held_bytes(a.v, lo[e], len[e], held[e]);
     __syncthreads();
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
@@ -390,28 +393,40 @@ __global__ __launch_bounds__(kThreads) void k_advance(GrammarArgs a, const int32
                                                       int B, int L, int32_t* out, int32_t* last) {
   __shared__ uint16_t lds[kEntries ? kEntries : 1];
   __shared__ uint16_t column[256];
-  const Table<kEntries, false> table(a.g, lds);
-  columns_of(a.g, column);
-  __syncthreads();
   const int lane = __lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int b = blockIdx.x * kWaves + wave;
+  // the tokens' loads go ahead of the table's
+  int from = -1, n = 0;
+  Token t = {};
+  if (b < B) {
+    from = states[b];
+    n = lens ? lens[b] : L;
+    n = n < 0 ? 0 : n > L ? L : n;
+    t = token_of(a.v, lane < n ? tokens[(size_t)b * L + lane] : -1);
+  }
+  const Table<kEntries, false> table(a.g, lds);
+  columns_of(a.g, column);
+  __syncthreads();
   if (b >= B) return;
-  const int from = states[b];
   const bool in = from >= 0 && from < a.g.n_states;
   int s = in ? table.at(from) : table.dead();
-  int n = lens ? lens[b] : L;
-  n = n < 0 ? 0 : n > L ? L : n;
   out += (size_t)b * (L + 1);
   if (lane == 0) out[0] = in ? from : -1;
   for (int i0 = 0; i0 < L; i0 += kWave) {
     const int held = n - i0 < kWave ? n - i0 : kWave;  // may be 0 or less
-    const Token t = token_of(a.v, lane < held ? tokens[(size_t)b * L + i0 + lane] : -1);
-    uint32_t columns[kHeld / 2];  // of its first bytes, two to a word
+    if (i0 > 0) t = token_of(a.v, lane < held ? tokens[(size_t)b * L + i0 + lane] : -1);
+    // its first bytes' columns, two to a word; a token with a byte that every
+    // state refuses counts as one without bytes
+    uint32_t columns[kHeld / 2];
+    bool refused = false;
 #pragma unroll
-    for (int k = 0; k < kHeld; k += 2)
-      columns[k / 2] = column[t.bytes[k]] | (uint32_t)column[t.bytes[k + 1]] << 16;
-    auto step = [&](int c) { return c == kRefused ? table.dead() : table.step(s, c); };
+    for (int k = 0; k < kHeld; k += 2) {
+      const uint32_t c0 = column[t.bytes[k]], c1 = column[t.bytes[k + 1]];
+      refused |= (k < t.len && c0 == kRefused) || (k + 1 < t.len && c1 == kRefused);
+      columns[k / 2] = c0 | c1 << 16;
+    }
+    if (refused) t.len = 0;
     int mine = table.dead();
     for (int i = 0; i < held && s != table.dead(); ++i) {
       const int len = lane_read(t.len, i);
@@ -421,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void k_advance(GrammarArgs a, const int32
       }
       until<kHeld>([&](auto k) {
         const uint32_t c = lane_read(columns[k / 2], i);
-        s = step(k % 2 ? c >> 16 : c & 0xFFFF);
+        s = table.step(s, k % 2 ? c >> 16 : c & 0xFFFF);
         return k + 1 < len;
       });
       if (len > kHeld) {
@@ -429,7 +444,10 @@ __global__ __launch_bounds__(kThreads) void k_advance(GrammarArgs a, const int32
         for (int k0 = kHeld; k0 < len && s != table.dead(); k0 += kWave) {
           // the next 64 bytes' columns, one a lane
           const int c = k0 + lane < len ? column[a.v.bytes[lo + k0 + lane]] : kRefused;
-          for (int k = 0; k < kWave && k0 + k < len; ++k) s = step(lane_read(c, k));
+          for (int k = 0; k < kWave && k0 + k < len; ++k) {
+            const int next = lane_read(c, k);
+            s = next == kRefused ? table.dead() : table.step(s, next);
+          }
         }
       }
       s = __builtin_amdgcn_readfirstlane(s);
