@@ -19,6 +19,7 @@ namespace {
 
 constexpr int64_t kWantedWaves = 8192;  // two for each place of a wave in the card's SIMDs
 constexpr int kGridY = 32768;           // sessions of a launch
+constexpr int kXcds = 8;
 constexpr int kBatch = 4;               // logits of a lane in flight, in place
 constexpr int kTurns = 4;               // turns over a tile's listed tokens whose reads overlap
 
@@ -66,6 +67,12 @@ struct Lanes {
   static constexpr int kE = 16 / (int)sizeof(T);  // logits of a vector
   static constexpr int kGroup = kWave * kE;       // logits of a group
 };
+
+// Groups of a tile, which holds kSize * 512 logits.
+template <typename T>
+constexpr int groups(int size) {
+  return size * (int)sizeof(T) / 2;
+}
 
 __device__ inline void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -178,27 +185,35 @@ constexpr uint32_t kBias = 0x8000;  // it has a bias
 // One wave, a workgroup of its own, works on kTile neighbouring tokens of one
 // session, row after row.  What the rows share is set up once, in LDS: the list
 // of the tokens that the history, a bias or a drafted token touches, and an
-// additive term for each.  Then the rows stream in 16-byte vectors, the next
-// row's on the way while this one is worked on; vectors that hold listed tokens
-// pass through LDS, where one lane a listed token changes it, and vectors with
-// an empty mask are not read.  In place, rows without a mask move their listed
-// tokens alone, lanes spread over tokens and rows.
+// additive term for each.  Then the rows stream in 16-byte vectors; vectors that
+// hold listed tokens pass through LDS, where one lane a listed token changes it,
+// and vectors with an empty mask are not read.  In place, rows without a mask
+// move their listed tokens alone, lanes spread over tokens and rows.
 //
-// What bounds it: out of place, HBM (188 us at B=256, M=8, V=128256 bf16 with
-// every rule: 1.2 GB at 6.3 TB/s; 61 us for one binary32 row of 256 sessions,
-// V=129280).  In place, the same sessions without masks take 98 us for 0.18 GB
-// of scattered 64-byte pieces, and the chain of dependent loads (controls,
-// history bits, counts, logits) of about 8 us a wave.
-// Why so: lanes that each work out their own vector's changes take 200 vector
-// instructions a row and tile against 60 here, which bound the kernel in place;
-// with workgroups of four waves, LDS stays held until the last one ends (253
-// and 202 us of then); loads and stores are non-temporal because the rows are
-// met once (198 and 188 us; the acceptance step that reads them afterwards is
-// 15% faster too).
-template <typename T, int G, bool kInPlace, bool kMasks>
+// What bounds it.  Out of place, HBM: 159 us at B=256, M=8, V=128256 bf16 with
+// every rule, where half the masks leave a few tokens (0.58 GB written, 0.16 to
+// 0.6 GB read); 61 us for one binary32 row of 256 sessions at V=129280 (277 MB,
+// 4.5 TB/s).  In place, the same 256 sessions without masks take 97 us for 0.18
+// GB in scattered 64-byte pieces, which two vectors a lane or more rows in
+// flight do not shorten.  Small batches, the chain of dependent loads
+// (controls; history bits, masks, biases; counts; logits), 5 us.
+// Why so.
+//  - Lanes that each work out their own vector's changes take 200 vector
+//    instructions a row and tile against 60 here; in place they were the bound.
+//  - All of a session's controls come with three loads, and everything that
+//    hangs on them alone with the next few: one after another, they made a wave
+//    wait 13 us.
+//  - Workgroups of four waves hold their LDS until the last one ends: 253 us
+//    where single waves took 202.
+//  - Loads and stores are non-temporal, since a row is met once: 202 to 188 us,
+//    and the acceptance step that reads the rows next is 15% faster too.
+//  - The next row's vectors and the mask of the row after it are on the way while
+//    a row is worked on, with no load passed over, so that the compiler's waits
+//    are for single loads: 188 to 159 us.
+template <typename T, int kSize, bool kInPlace, bool kMasks>
 __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
   using L = Lanes<T>;
-  constexpr int E = L::kE, kTile = G * L::kGroup;
+  constexpr int G = groups<T>(kSize), E = L::kE, kTile = G * L::kGroup;
   constexpr uint32_t kAll = (1u << E) - 1;  // one vector's tokens
   constexpr uint32_t kFull = G * E == 32 ? ~0u : (1u << (G * E)) - 1;
   static_assert(G * E <= 32 && kTile <= (int)kPlace + 1, "a lane's tokens fit one word");
@@ -208,7 +223,15 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
   __shared__ uint16_t list[kTile];
   __shared__ uint32_t bits[kTile / 32];
   const int lane = __lane_id();
-  const int tile = blockIdx.x, v0 = tile * kTile;
+  int tile = blockIdx.x;
+  if constexpr (kSize == 2) {
+    // uneven rows: neighbouring tiles to one XCD (workgroups go to them in turn),
+    // whose L2 then has the lines that they share (197 to 191 us for 192 sessions
+    // of up to 17 rows, V=151935; even rows lose 2% by it)
+    const int nth = tile % kXcds, each = gridDim.x / kXcds, over = gridDim.x % kXcds;
+    tile = nth * each + min(nth, over) + tile / kXcds;
+  }
+  const int v0 = tile * kTile;
   const int first = lane * E;   // a lane's vectors start at first + g * kGroup
   const int left = a.V - v0;    // tokens from the tile's start to the row's end
   const int chunk = blockIdx.z;
@@ -581,10 +604,11 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
 
 template <typename T, int kSize, bool kInPlace, bool kMasks>
 void launch(AdjustArgs a, hipStream_t st) {
-  constexpr int G = kSize * (int)sizeof(T) / 2, kTile = G * Lanes<T>::kGroup;
+  constexpr int kTile = groups<T>(kSize) * Lanes<T>::kGroup;
   const int64_t tiles = (a.V + kTile - 1) / kTile;
   // rows go to several waves where a wave per tile would leave the card idle; a
-  // quarter as many where rows move their listed tokens alone
+  // quarter as many where rows move their listed tokens alone and the setup is
+  // most of the work
   const int64_t wanted = kInPlace && !kMasks ? kWantedWaves / 4 : kWantedWaves;
   int64_t chunks = (wanted + tiles * a.B - 1) / (tiles * a.B);
   chunks = chunks < a.R ? chunks : a.R;
@@ -592,15 +616,15 @@ void launch(AdjustArgs a, hipStream_t st) {
   chunks = (a.R + a.chunk - 1) / a.chunk;
   for (a.b0 = 0; a.b0 < a.B; a.b0 += kGridY) {
     const dim3 grid((unsigned)tiles, a.B - a.b0 < kGridY ? a.B - a.b0 : kGridY, (unsigned)chunks);
-    hipLaunchKernelGGL((k_adjust<T, G, kInPlace, kMasks>), grid, dim3(kWave), 0, st, a);
+    hipLaunchKernelGGL((k_adjust<T, kSize, kInPlace, kMasks>), grid, dim3(kWave), 0, st, a);
   }
 }
 
 // One vector of a row per lane, or two.  One lets twice the waves share the LDS:
-// 54.7 against 60.5 us at B=128, R=17, V=32000 and 176 against 182 us at
+// 52.0 against 56.1 us at B=128, R=17, V=32000 and 165 against 174 us at
 // V=128256 (bf16, penalties and masks).  Where rows start off a 16-byte
 // boundary every tile's ends share cache lines with its neighbours', and two
-// vectors have half as many ends: 208 against 221 us at V=128255.
+// vectors have half as many ends: 209 against 221 us at V=128255.
 template <typename T>
 void launch(const AdjustArgs& a, hipStream_t st) {
   constexpr int E = Lanes<T>::kE;

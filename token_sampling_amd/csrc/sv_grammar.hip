@@ -170,8 +170,8 @@ __device__ inline Token token_of(const sv_vocab& v, int id) {
   return t;
 }
 
-// Masks of states over a tile of kTile tokens, which a workgroup holds in LDS,
-// its tokens ordered by their first column.
+// Masks of states over a tile of kTile tokens, which a workgroup holds in LDS
+// with the automaton, its tokens ordered by their first column.
 //
 // A state of a grammar mostly goes on from one byte in a hundred, so nearly all
 // walks would end at their first byte.  A wave takes one state at a time and
@@ -179,11 +179,19 @@ __device__ inline Token token_of(const sv_vocab& v, int id) {
 // neighbouring columns together, 64 tokens abreast; those that are allowed set
 // their bit in the wave's words in LDS, which then go out whole.  Waves take
 // states as they become free, since some (inside a string) allow most tokens.
-// With a lane for each token and state instead, 1500 states over 128256 tokens
-// took 309 us, most of it on walks that ended at once.
+//
+// 1500 states of an automaton of 1474 by 37, V=128256: 66 us, bound by issue
+// (218 vector, 94 scalar and 50 LDS instructions a state and tile), 24 MB
+// written.  20 states, V=32000: 12.6 us, the table's and the tokens' loads and
+// one state that allows most of a tile.  Steps: a lane for each token and state,
+// the table in global memory, 803 us; in LDS, four states abreast, 309; tokens by
+// first column within 1024, a wave's states tested together, 186; this order with
+// a test of each token's length in each step, 115; the end() column instead, 66.
+// Tokens longer than kHeld bytes have a run of their own: finished one by one
+// inside the others', they took as long as all the rest.
 constexpr int kTile = 2048;
-constexpr int kStates = 512;   // states that a workgroup has at hand
-constexpr int kAbreast = 4;     // 64s of tokens whose lookups overlap
+constexpr int kStates = 512;  // states that a workgroup has at hand
+constexpr int kAbreast = 4;   // 64s of tokens whose lookups overlap (2: 71, 8: 65 us of then 65)
 template <int kEntries, int kParts>
 __global__ __launch_bounds__(kThreads) void k_masks(GrammarArgs a, const int32_t* states, int n,
                                                     int part, uint32_t* bits) {
@@ -387,8 +395,11 @@ __global__ __launch_bounds__(kThreads) void k_masks(GrammarArgs a, const int32_t
 
 // A session's tokens: a wave holds 64 of them, one a lane, and walks them one
 // after another, every lane alike; the chain of lookups is what it waits for.
+// 8 drafts of 256 sessions: 8.6 us, of which 4 to bring a table of 109 KB to
+// LDS; 64 drafts of 1024 sessions, up to 400 bytes each: 18.8 us.  One lane a
+// session with the table in global memory took 16 and 103 us.
 template <int kEntries>
-__global__ __launch_bounds__(kThreads) void k_advance(GrammarArgs a, const int32_t* states,
+__global__ __launch_bounds__(kThreads) void k_walk(GrammarArgs a, const int32_t* states,
                                                       const int32_t* tokens, const int32_t* lens,
                                                       int B, int L, int32_t* out, int32_t* last) {
   __shared__ uint16_t lds[kEntries ? kEntries : 1];
@@ -520,7 +531,7 @@ extern "C" int sv_grammar_advance(const sv_grammar* grammar, const sv_vocab* voc
   GrammarArgs a = {*grammar, *vocab};
   (void)hipGetLastError();
   by_size(*grammar, [&](auto entries) {
-    hipLaunchKernelGGL(k_advance<decltype(entries)::value>, dim3((B + kWaves - 1) / kWaves),
+    hipLaunchKernelGGL(k_walk<decltype(entries)::value>, dim3((B + kWaves - 1) / kWaves),
                        dim3(kThreads), 0, (hipStream_t)stream, a, states, tokens, lens, B, L,
                        out_states, last);
   });
