@@ -53,7 +53,7 @@ extern "C" {
 #define SV_V_MAX (1 << 24)   /* largest vocabulary accepted */
 #define SV_B_MAX (1 << 21)   /* most sessions per call */
 #define SV_SLOTS_MAX (1 << 25) /* most row slots B * (2M + 1) per call */
-#define SV_BIAS_MAX (1 << 30)  /* most bias entries per call */
+#define SV_ENTRIES_MAX (1 << 30) /* most bias entries, vocabulary bytes or states per call */
 
 /* Per-session sampling profile (SDCP Sec. 4.1 "sampling"), 24 bytes,
  * 8-byte aligned; passed as a DEVICE array [B]. */
@@ -416,7 +416,7 @@ typedef struct sv_history {
 
 /* Sparse biases: session b has entries offsets[b] .. offsets[b+1]-1 of ids
  * (strictly ascending within a session; ids outside [0, V) have no effect) and
- * values.  A HOST struct of DEVICE pointers. */
+ * values, at most SV_ENTRIES_MAX in all.  A HOST struct of DEVICE pointers. */
 typedef struct sv_bias {
   const int32_t *offsets; /* [B + 1] */
   const int32_t *ids;     /* [n] */
@@ -507,7 +507,8 @@ typedef struct sv_grammar {
 } sv_grammar;
 
 /* The tokens' bytes: token v's are bytes[offsets[v]] .. bytes[offsets[v+1]-1];
- * none for control tokens.  end: up to SV_STOP_MAX tokens that end a text
+ * none for control tokens; at most SV_ENTRIES_MAX bytes in all (offsets that
+ * leave them are cut).  end: up to SV_STOP_MAX tokens that end a text
  * (their bytes, if any, do not count).  A HOST struct of DEVICE pointers. */
 typedef struct sv_vocab {
   const uint8_t *bytes;   /* [n_bytes] */
@@ -521,7 +522,7 @@ typedef struct sv_vocab {
  * a state of the automaton a token is allowed if it has bytes and none of them
  * is refused, an end token if the state accepts, another token without bytes
  * never.  For states outside [0, n_states) (-1: no grammar) every token is
- * allowed.  Returns SV_OK, SV_ERR_ARG (also n < 1) or SV_ERR_DEVICE.
+ * allowed.  1 <= n <= SV_ENTRIES_MAX.  Returns SV_OK, SV_ERR_ARG or SV_ERR_DEVICE.
  */
 int sv_grammar_masks(const sv_grammar *grammar, const sv_vocab *vocab, const int32_t *states,
                      int32_t n, uint32_t *bits, void *stream);

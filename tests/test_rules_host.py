@@ -96,8 +96,8 @@ def test_count_refuses(bad):
 
 @pytest.mark.parametrize("bad", [
     dict(next=None), dict(classes=None), dict(accept=None), dict(S=0), dict(C=0), dict(C=257),
-    dict(offsets=None), dict(bytes=None), dict(n_bytes=-1), dict(n_end=9), dict(n_end=-1),
-    dict(end=None), dict(V=0), dict(V=(1 << 24) + 1), dict(states=None), dict(out=None), dict(n=0)], ids=str)
+    dict(offsets=None), dict(bytes=None), dict(n_bytes=-1), dict(n_bytes=(1 << 30) + 1), dict(n_end=9), dict(n_end=-1),
+    dict(end=None), dict(V=0), dict(V=(1 << 24) + 1), dict(states=None), dict(out=None), dict(n=0), dict(n=(1 << 30) + 1)], ids=str)
 def test_grammar_refuses(bad):
     a = dict(next=FAKE, classes=FAKE, accept=FAKE, S=2, C=3, bytes=FAKE, offsets=FAKE, end=FAKE, n_bytes=9,
              n_end=1, V=4, states=FAKE, out=FAKE, n=2)

@@ -653,8 +653,8 @@ def make_vocab(tokens, end=(), device="cuda"):
         raise ValueError("end must hold at most 8 ids of the vocabulary")
     offsets = np.zeros(len(tokens) + 1, np.int64)
     np.cumsum([len(t) for t in tokens], out=offsets[1:])
-    if offsets[-1] >= 1 << 31:
-        raise ValueError("the tokens' bytes exceed 2 GiB")
+    if offsets[-1] > 1 << 30:
+        raise ValueError("the tokens' bytes exceed 1 GiB")
     flat = np.frombuffer(b"".join(tokens), dtype=np.uint8)
     return Vocab(torch.from_numpy(flat.copy()).to(device),
                  torch.from_numpy(offsets.astype(np.int32)).to(device),

@@ -666,7 +666,7 @@ extern "C" int sv_adjust_logits(const void* logits, int64_t session_stride, int6
   if (history && (!history->counts || !history->seen || history->n_slots < 1 ||
                   (!slots && history->n_slots < B)))
     return SV_ERR_ARG;
-  if (bias && (!bias->offsets || bias->n < 0 || bias->n > SV_BIAS_MAX || (bias->n > 0 && (!bias->ids || !bias->values))))
+  if (bias && (!bias->offsets || bias->n < 0 || bias->n > SV_ENTRIES_MAX || (bias->n > 0 && (!bias->ids || !bias->values))))
     return SV_ERR_ARG;
   if (masks && (!masks->bits || !masks->rows || masks->n_masks < 1)) return SV_ERR_ARG;
   AdjustArgs a = {};

@@ -400,8 +400,8 @@ __global__ __launch_bounds__(kThreads) void k_masks(GrammarArgs a, const int32_t
 // session with the table in global memory took 16 and 103 us.
 template <int kEntries>
 __global__ __launch_bounds__(kThreads) void k_walk(GrammarArgs a, const int32_t* states,
-                                                      const int32_t* tokens, const int32_t* lens,
-                                                      int B, int L, int32_t* out, int32_t* last) {
+                                                   const int32_t* tokens, const int32_t* lens,
+                                                   int B, int L, int32_t* out, int32_t* last) {
   __shared__ uint16_t lds[kEntries ? kEntries : 1];
   __shared__ uint16_t column[256];
   const int lane = __lane_id();
@@ -481,7 +481,7 @@ bool grammar_ok(const sv_grammar* g, const sv_vocab* v) {
   if (!g || !g->next || !g->classes || !g->accept || g->n_states < 1 || g->n_classes < 1 ||
       g->n_classes > 256)
     return false;
-  if (!v || !v->offsets || v->n_bytes < 0 || (v->n_bytes > 0 && !v->bytes) || v->n_end < 0 ||
+  if (!v || !v->offsets || v->n_bytes < 0 || v->n_bytes > SV_ENTRIES_MAX || (v->n_bytes > 0 && !v->bytes) || v->n_end < 0 ||
       v->n_end > SV_STOP_MAX || (v->n_end > 0 && !v->end) || v->V < 1 || v->V > SV_V_MAX)
     return false;
   return true;
@@ -493,7 +493,8 @@ bool grammar_ok(const sv_grammar* g, const sv_vocab* v) {
 extern "C" int sv_grammar_masks(const sv_grammar* grammar, const sv_vocab* vocab,
                                 const int32_t* states, int32_t n, uint32_t* bits, void* stream) {
   using namespace sv;
-  if (!grammar_ok(grammar, vocab) || !states || !bits || n < 1) return SV_ERR_ARG;
+  if (!grammar_ok(grammar, vocab) || !states || !bits || n < 1 || n > SV_ENTRIES_MAX)
+    return SV_ERR_ARG;
   GrammarArgs a = {*grammar, *vocab};
   (void)hipGetLastError();
   by_size(*grammar, [&](auto entries) {
