@@ -175,3 +175,70 @@ def test_a_failed_session_is_not_sampled():
     torch.cuda.synchronize()
     assert got["status"].tolist() == [0, 0, sv.S_BAD_CONTROL, 0]
     assert res["accepted_len"][2] == sv.S_BAD_LOGITS and (res["accepted_len"][[0, 1, 3]] >= 0).all()
+
+
+def chain(seed, stream=None):
+    """One batch's states, masks, adjusted rows and history; its results."""
+    rng = np.random.default_rng(seed)
+    B, M, V = 20, 6, 9000 + seed
+    nxt, accept = ref.random_grammar(rng, 40, 25, live=0.9)
+    tokens = ref.random_vocab(rng, V)
+    g, v = sv.make_grammar(nxt, accept), sv.make_vocab(tokens, [3])
+    at = dev(rng.integers(-1, 40, B).astype(np.int32))
+    drafts = dev(rng.integers(0, V, (B, M)).astype(np.int32))
+    m = dev(rng.integers(0, M + 1, B).astype(np.int32))
+    logits = torch.randn((B, M + 1, V), device="cuda", generator=torch.Generator("cuda").manual_seed(seed)).bfloat16()
+    history, pen = sv.make_history(B, V), sv.make_penalties(B, 1.2, 0.3, 0.1)
+    out, status = torch.zeros_like(logits), torch.empty(B, dtype=torch.int32, device="cuda")
+    states = {"states": torch.empty((B, M + 1), dtype=torch.int32, device="cuda"),
+              "last": torch.empty(B, dtype=torch.int32, device="cuda")}
+    bits = torch.empty((B * (M + 1), (V + 31) // 32), dtype=torch.int32, device="cuda")
+    rows = torch.arange(B * (M + 1), dtype=torch.int32, device="cuda").view(B, M + 1)
+    torch.cuda.synchronize()
+
+    def go():
+        sv.count_tokens(history, drafts, lens=m, clear=True, stream=stream)
+        sv.grammar_advance(g, v, at, drafts, lens=m, out=states, stream=stream)
+        sv.grammar_masks(g, v, states["states"].view(-1), out=bits, stream=stream)
+        sv.adjust_logits(logits, tokens=drafts, m=m, penalties=pen, history=history, masks=bits, mask_rows=rows,
+                         out=out, status=status, stream=stream)
+        return [t.clone() for t in (out.view(torch.int16), status, states["states"], bits, history.counts, history.seen)]
+
+    return go
+
+
+def test_two_streams_at_once():
+    want = [chain(s)() for s in (1, 2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    runs = [chain(s, st) for s, st in zip((1, 2), streams)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for go, st in zip(runs, streams):
+            with torch.cuda.stream(st):
+                got = go()
+            go.got = got
+    torch.cuda.synchronize()
+    for go, w in zip(runs, want):
+        assert all(torch.equal(a, b) for a, b in zip(go.got, w))
+        assert (w[1] == 0).all()
+
+
+def test_two_graphs_in_turn():
+    """Two captured batches replayed in turn and together with eager calls."""
+    runs = [chain(s) for s in (3, 4)]
+    want = [go() for go in runs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for go in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(go())
+        graphs.append(g)
+    for r in range(4):
+        for g, o, go, w in zip(graphs, outs, runs, want):
+            g.replay()
+            eager = go()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(o, w)), r
+            assert all(torch.equal(a, b) for a, b in zip(eager, w)), r
