@@ -20,6 +20,10 @@ namespace {
 // Waves to fill the card with, half its places (B=64, R=5, V=32000: 12.5 us, with
 // 8192 14.2; B=64, R=65, V=1300: 18.2 and 17.7).
 constexpr int64_t kWantedWaves = 4096;
+// Most rows of a wave that streams them: longer ones end late (192 sessions of up
+// to 17 rows, V=151935: 184 us, uncut 191, by 6 rows 191; 32 sessions of 65 rows,
+// V=128256: 177, uncut 193).
+constexpr int kMostRows = 9;
 constexpr int kGridY = 32768;           // sessions of a launch
 constexpr int kXcds = 8;
 constexpr int kBatch = 4;               // logits of a lane in flight, in place
@@ -613,6 +617,10 @@ void launch(AdjustArgs a, hipStream_t st) {
   // work
   const int64_t wanted = kInPlace && !kMasks ? kWantedWaves / 2 : kWantedWaves;
   int64_t chunks = (wanted + tiles * a.B - 1) / (tiles * a.B);
+  if (!kInPlace || kMasks) {
+    const int64_t least = (a.R + kMostRows - 1) / kMostRows;
+    chunks = chunks > least ? chunks : least;
+  }
   chunks = chunks < a.R ? chunks : a.R;
   a.chunk = (int)((a.R + chunks - 1) / chunks);
   chunks = (a.R + a.chunk - 1) / a.chunk;
