@@ -193,8 +193,9 @@ constexpr uint32_t kBias = 0x8000;  // it has a bias
 // of the tokens that the history, a bias or a drafted token touches, and an
 // additive term for each.  Then the rows stream in 16-byte vectors; vectors that
 // hold listed tokens pass through LDS, where one lane a listed token changes it,
-// and vectors with an empty mask are not read.  In place, rows without a mask
-// move their listed tokens alone, lanes spread over tokens and rows.
+// and vectors with an empty mask are not read.  In place, the vectors that change
+// move; where the call has no masks, listed tokens alone, lanes spread over tokens
+// and rows.
 //
 // What bounds it.  Out of place, HBM: 159 us at B=256, M=8, V=128256 bf16 with
 // every rule, where half the masks leave a few tokens (0.58 GB written, 0.16 to
@@ -311,10 +312,11 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
 
   // The same for a tile that the row has all of, rows past the last included:
   // vectors that are not needed come from nothing, so that every lane loads.
-  [[maybe_unused]] auto load_whole = [&](int r, uint32_t mk, u32x4 (&x)[G]) {
+  [[maybe_unused]] auto load_whole = [&](int r, uint32_t mk, uint32_t needed, u32x4 (&x)[G]) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const bool wanted = r < r1 && ((mk >> (g * E)) & kAll) != 0;
+      const bool wanted = r < r1 && ((mk >> (g * E)) & kAll) != 0 &&
+                          ((needed >> (g * E)) & kAll) != 0;
       x[g] = load16(wanted ? in + r * a.in_row + g * L::kGroup + first : (const T*)nothing);
     }
   };
@@ -362,7 +364,7 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
   if constexpr (!kInPlace) ahead = mask_ahead(r0 + 1);
   uint32_t mk = mask0 < 0 ? kFull : packed(mask);
   if constexpr (!kInPlace) {
-    if (left >= kTile) load_whole(r0, mk, x);
+    if (left >= kTile) load_whole(r0, mk, kFull, x);
     else load(r0, mk, kFull, x);
   }
 
@@ -534,16 +536,23 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     }
   };
 
-  if constexpr (!kInPlace) {
+  // the vectors of a row that move: in place, those that change (any has a bit
+  // for each listed token)
+  [[maybe_unused]] auto moved = [&](uint32_t ok) { return kInPlace ? any | (ok ^ kFull) : kFull; };
+  if constexpr (kVectors) {
     if (left >= kTile) {
       // two rows in turn, the next one's loads on the way while one is worked on;
       // no load or store is passed over, so that each wait is for its own
+      if constexpr (kInPlace) {
+        ahead = mask_ahead(r0 + 1);
+        load_whole(r0, mk, moved(mk), x);
+      }
       __builtin_amdgcn_s_waitcnt(0);
       auto half = [&](int r, u32x4 (&x0)[G], uint32_t m0, u32x4 (&x1)[G], uint32_t& m1) {
         if (r > r0 && ((mine >> (r - 1)) & 1)) meet(r - 1);
         m1 = ahead_of(ahead);
         ahead = mask_ahead(r + 2);
-        load_whole(r + 1, m1, x1);
+        load_whole(r + 1, m1, moved(m1), x1);
         finish(r, m0, x0, std::true_type());
       };
       u32x4 x1[G];
@@ -590,10 +599,9 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     }
     if constexpr (kVectors) {
       const uint32_t next = mask_of(mask_row(r + 1));
-      // in place: the vectors that change (any has a bit for each listed token)
       if constexpr (kInPlace) {
         mk = mask_of(mask_row(r));
-        load(r, mk, any | (mk ^ kFull), x);
+        load(r, mk, moved(mk), x);
       }
       u32x4 y[G];
 #pragma unroll
