@@ -197,7 +197,7 @@ constexpr uint32_t kBias = 0x8000;  // it has a bias
 // move; where the call has no masks, listed tokens alone, lanes spread over tokens
 // and rows.
 //
-// What bounds it.  Out of place, HBM: 160 us at B=256, M=8, V=128256 bf16 with
+// What bounds it.  Out of place, HBM: 159 to 164 us at B=256, M=8, V=128256 bf16 with
 // every rule, where half the masks leave a few tokens (0.58 GB written, 0.16 to
 // 0.6 GB read); 61 us for one binary32 row of 256 sessions at V=129280 (277 MB,
 // 4.5 TB/s).  In place, the same 256 sessions without masks take 97 us for 0.18
