@@ -451,8 +451,9 @@ typedef struct sv_masks {
  *           session_stride + r * row_stride (both >= 0), its V logits are
  *           contiguous;
  *   out     DEVICE [B, R, V] contiguous, not overlapping logits; or logits
- *           itself (in place: only logits that change are written, and the
- *           strides must keep the used rows apart);
+ *           itself (in place: only logits that change are written, and no two
+ *           of the B * R rows may overlap, used or not, or the call is refused:
+ *           a failed session's rows are all written);
  *   draft_tokens [B, M] int32 (NULL only if M == 0 or penalties == NULL), m
  *           [B] int32 with 0 <= m[b] <= M, or NULL for m[b] = M;
  *   penalties [B], history, bias, masks: each may be NULL (that rule is off);

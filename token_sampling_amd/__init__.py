@@ -734,7 +734,7 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
     [n, W] int32 bit rows (make_masks, grammar_masks) with mask_rows [B, R] int32
     (-1: no mask).
     out: None for a new contiguous tensor; a contiguous one like it; or logits
-    itself (in place, the rows then must not overlap).  Rows that a session does
+    itself (in place, no two of its B * R rows may then overlap).  Rows that a session does
     not use are not written.  Returns dict(logits=out, status=[B] int32: 0, or
     why a session failed, whose rows are then NaN).
     """
@@ -797,11 +797,8 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
             lo, hi = logits.data_ptr(), logits.data_ptr() + ((B - 1) * sb + (R - 1) * sr + V) * logits.element_size()
             if out.data_ptr() < hi and lo < out.data_ptr() + out.numel() * out.element_size():
                 raise ValueError("out overlaps logits")
-        if out.data_ptr() == logits.data_ptr():
-            near, far = sorted(((sb, B), (sr, R)))
-            if (far[1] > 1 and far[0] < V) or (near[1] > 1 and near[0] < V) or \
-                    (far[1] > 1 and far[0] < (near[1] - 1) * near[0] + V):
-                raise ValueError("rows overlap: logits cannot be adjusted in place")
+        if out.data_ptr() == logits.data_ptr() and not _rows_apart(sb, sr, B, R, V):
+            raise ValueError("rows overlap: logits cannot be adjusted in place")
         if status is None:
             status = torch.empty(B, dtype=torch.int32, device=dev)
         else:
@@ -812,6 +809,23 @@ def adjust_logits(logits, tokens=None, m=None, penalties=None, history=None, slo
     if rc != OK:
         raise SvError(f"sv_adjust_logits failed: {strerror(rc)} ({rc})")
     return {"logits": out, "status": status}
+
+
+def _rows_apart(sb, sr, B, R, V):
+    """Whether no two of the B * R rows that start at b * sb + r * sr share one of
+    their V logits."""
+    near, far = sorted(((sb, B), (sr, R)))
+    if near[1] == 1:  # all rows at one stride
+        return far[1] == 1 or far[0] >= V
+    if near[0] < V or (far[1] > 1 and far[0] < V):
+        return False
+    width = (near[1] - 1) * near[0] + V
+    # the near stride's multiples on both sides of d far strides, as far as they reach
+    for d in range(1, min(far[1], (width - 1) // far[0] + 1)):
+        q = min(d * far[0] // near[0], near[1] - 1)
+        if d * far[0] - q * near[0] < V or (q + 1 < near[1] and (q + 1) * near[0] - d * far[0] < V):
+            return False
+    return True
 
 
 def _check_like(out, logits):

@@ -662,6 +662,20 @@ void launch(const AdjustArgs& a, hipStream_t st) {
   }
 }
 
+// Whether no two of the B * R rows of V logits share one: in place, each is written
+// by waves of its own.  Rows dr apart within their sessions come nearest where
+// the sessions' distance is just below dr * row_stride, or just above it.
+bool rows_apart(int64_t session_stride, int64_t row_stride, int B, int R, int V) {
+  if (B > 1 && session_stride < V) return false;
+  for (int dr = 1; dr < R; ++dr) {
+    const int64_t x = dr * row_stride;
+    const int64_t db = B == 1 ? 0 : x / session_stride < B ? x / session_stride : B - 1;
+    if (x - db * session_stride < V) return false;
+    if (db + 1 < B && (db + 1) * session_stride - x < V) return false;
+  }
+  return true;
+}
+
 }  // namespace
 }  // namespace sv
 
@@ -680,6 +694,7 @@ extern "C" int sv_adjust_logits(const void* logits, int64_t session_stride, int6
   if (session_stride < 0 || row_stride < 0 || session_stride > (int64_t)1 << 40 ||
       row_stride > (int64_t)1 << 40)
     return SV_ERR_ARG;
+  if (out == logits && !rows_apart(session_stride, row_stride, B, R, V)) return SV_ERR_ARG;
   if (M > 0 && penalties && !draft_tokens) return SV_ERR_ARG;
   if (history && (!history->counts || !history->seen || history->n_slots < 1 ||
                   (!slots && history->n_slots < B)))
