@@ -601,14 +601,17 @@ def make_bias(biases, V, device="cuda"):
         for t in sorted(d or ()):
             if not 0 <= t < V:
                 raise ValueError(f"bias for token {t}, outside the vocabulary of {V}")
-            if not d[t] < float("inf"):
-                raise ValueError(f"bias of token {t} must be finite or -inf")
             ids.append(t)
             values.append(d[t])
         offsets.append(len(ids))
+    with np.errstate(over="ignore"):
+        packed = np.asarray(values, dtype=np.float64).astype(np.float32)
+    for t, x in zip(ids, packed):  # as they will be added: a large double is an infinity here
+        if not x < np.inf:
+            raise ValueError(f"bias of token {t} must be -inf or finite in binary32")
     return Bias(torch.tensor(offsets, dtype=torch.int32).to(device),
                 torch.tensor(ids, dtype=torch.int32).to(device),
-                torch.tensor(values, dtype=torch.float32).to(device))
+                torch.from_numpy(packed).to(device))
 
 
 def make_masks(allowed, device="cuda"):
