@@ -176,6 +176,10 @@ __device__ inline float from_bits(uint32_t x, float) { return __builtin_bit_cast
 template <typename T>
 constexpr uint32_t kMinusInf = sizeof(T) == 2 ? 0xFF80FF80u : 0xFF800000u;
 
+// What a token without a bias has for one: -0, which leaves every logit as it is (+0
+// would make a logit of -0 another).
+constexpr float kNoBias = -0.f;
+
 // What a token's logit gets added: its bias, less its penalties at count c.
 __device__ inline float term_of(const Session& s, float bias, int c) {
   return c > 0 ? bias - fmaf(s.frequency, (float)c, s.presence) : bias;
@@ -433,7 +437,7 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     for (int j = lane; j < listed; j += kWave) {
       uint32_t e = list[j];
       const int i = e & kPlace;
-      float t = e & kBias ? term[i] : 0.f;
+      float t = e & kBias ? term[i] : kNoBias;
       int c = e & kHad ? a.counts[(size_t)s.slot * a.V + v0 + i] : 0;
       if (early != 0) {
         const int more = early_count[i];
@@ -463,7 +467,7 @@ __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
     // the row its wave began with
     int c = __popcll(__ballot(s.token == v && lane <= d));
     if ((lane_read(had, owner) >> k) & 1) c += a.counts[(size_t)s.slot * a.V + v];
-    float t = 0.f;
+    float t = kNoBias;
     const uint32_t e = list[j];
     if (e & kBias)
       for (int i = bias_lo + lane; i < bias_hi; i += kWave)
