@@ -443,17 +443,23 @@ typedef struct sv_masks {
  *                                                          : z * repetition
  *   z = z - frequency * c - (c > 0 ? presence : 0) + bias(v)
  *   z = -inf where the row's mask has bit 0, whatever it was
- * rounded once to dtype; tokens that no rule changes keep their bits.  Rows a
- * session does not use are neither read nor written.  A mask that allows
+ * rounded once to dtype; tokens that no rule changes keep their bits.  The
+ * quotient is the product with the rounded 1 / repetition, and the penalties and
+ * bias(v) are summed before they meet z (an overflow of that sum is z's too):
+ * before it is rounded to dtype, z is off by at most 3 * 2^-24 of the sum of the
+ * magnitudes of its quotient or product, frequency * c, presence and bias(v).
+ * Rows a session does not use are neither read nor written.  A mask that allows
  * nothing leaves a row of -inf, which the acceptance step reports as
  * SV_S_BAD_LOGITS.
  *   logits  DEVICE, of dtype: row r of session b starts at element b *
  *           session_stride + r * row_stride (both >= 0), its V logits are
  *           contiguous;
  *   out     DEVICE [B, R, V] contiguous, not overlapping logits; or logits
- *           itself (in place: only logits that change are written, and no two
- *           of the B * R rows may overlap, used or not, or the call is refused:
- *           a failed session's rows are all written);
+ *           itself (in place: logits that do not change keep their bits, though
+ *           those that a rule looks at, and with masks their neighbours within
+ *           16 bytes, may be written again; no two of the B * R rows may
+ *           overlap, used or not, or the call is refused: a failed session's
+ *           rows are all written);
  *   draft_tokens [B, M] int32 (NULL only if M == 0 or penalties == NULL), m
  *           [B] int32 with 0 <= m[b] <= M, or NULL for m[b] = M;
  *   penalties [B], history, bias, masks: each may be NULL (that rule is off);
@@ -535,8 +541,10 @@ int sv_grammar_masks(const sv_grammar *grammar, const sv_vocab *vocab, const int
  * after a token that is not allowed or ends the text, and for i > lens[b].  A
  * round's row r takes the mask of out_states[b][r]: a drafted token that is not
  * allowed has probability zero in its own row, so its position rejects and the
- * rows after it, which carry no mask, do not count.  tokens [B, L] int32, lens
- * [B] (cut to [0, L]) or NULL for L.  last [B] or NULL: the state after all
+ * rows after it, which carry no mask, do not count.  A last state of -1 from
+ * another start means that a token was not allowed (it was committed without its
+ * mask) or ended the text; which, the token itself tells.  tokens [B, L] int32,
+ * lens [B] (cut to [0, L]) or NULL for L.  last [B] or NULL: the state after all
  * lens[b] tokens; last may be states.  1 <= B <= SV_B_MAX, 0 <= L <= 65.
  * Returns SV_OK, SV_ERR_ARG or SV_ERR_DEVICE.
  */
