@@ -6,7 +6,9 @@
 //   z = v seen ? (z > 0 ? z / rep : z * rep) : z
 //   z = z - freq * c - (c > 0 ? pres : 0) + bias(v)
 //   z = mask bit clear ? -inf : z
-// in binary32, rounded once to the logits' type.
+// in binary32, rounded once to the logits' type; as z * f + t, with f the rounded
+// 1 / rep or rep, and t the bias less the penalties (3 roundings of 2^-24 of the
+// terms' magnitudes at most).
 #include <limits.h>
 #include <math.h>
 
@@ -22,7 +24,10 @@ namespace {
 constexpr int64_t kWantedWaves = 4096;
 // Most rows of a wave that streams them: longer ones end late (192 sessions of up
 // to 17 rows, V=151935: 184 us, uncut 191, by 6 rows 191; 32 sessions of 65 rows,
-// V=128256: 177, uncut 193).
+// V=128256: 177, uncut 193).  Even rows cut in two set up twice, and gain or lose
+// little by it: 10, 12, 14, 16 rows of 256 sessions, V=128256, take 191, 218, 257,
+// 289 us, uncut 195, 218, 263, 295; of 1024 sessions, V=32000, 194, 228, 267, 285,
+// uncut 187, 225, 267, 290 (each +-2% from run to run).
 constexpr int kMostRows = 9;
 constexpr int kGridY = 32768;           // sessions of a launch
 constexpr int kXcds = 8;
@@ -201,13 +206,16 @@ constexpr uint32_t kBias = 0x8000;  // it has a bias
 // move; where the call has no masks, listed tokens alone, lanes spread over tokens
 // and rows.
 //
-// What bounds it.  Out of place, HBM: 159 to 164 us at B=256, M=8, V=128256 bf16 with
+// What bounds it.  Out of place, HBM: 159 to 165 us at B=256, M=8, V=128256 bf16 with
 // every rule, where half the masks leave a few tokens (0.58 GB written, 0.16 to
 // 0.6 GB read); 61 us for one binary32 row of 256 sessions at V=129280 (277 MB,
-// 4.5 TB/s).  In place, the same 256 sessions without masks take 97 us for 0.18
-// GB in scattered 64-byte pieces, which two vectors a lane or more rows in
-// flight do not shorten.  Small batches, the chain of dependent loads
-// (controls; history bits, masks, biases; counts; logits), 5 us.
+// 4.5 TB/s).  In place, the same 256 sessions without masks take 98 us for 0.18
+// GB in scattered 64-byte pieces; two vectors a lane, which also halve the waves
+// in flight, or more rows of a lane's in flight do not shorten it.  Its waves, 8 on
+// a SIMD, wait in 69% of their cycles: for the chain of their setup or for the
+// pieces, which the counters do not tell apart.  In place with masks, 180 us for
+// 706 MB.  Small batches, the chain of dependent loads (controls; history bits,
+// masks, biases; counts; logits), 5 us.
 // Why so.
 //  - Lanes that each work out their own vector's changes take 200 vector
 //    instructions a row and tile against 60 here; in place they were the bound.
@@ -221,6 +229,8 @@ constexpr uint32_t kBias = 0x8000;  // it has a bias
 //  - The next row's vectors and the mask of the row after it are on the way while
 //    a row is worked on, with no load passed over, so that the compiler's waits
 //    are for single loads: 188 to 159 us.
+// Scalar registers run out in the kernels of two vectors (4 spilled to lanes of a
+// vector register without masks, 13 with them) and in place with masks (10).
 template <typename T, int kSize, bool kInPlace, bool kMasks>
 __global__ __launch_bounds__(kWave) void k_adjust(AdjustArgs a) {
   using L = Lanes<T>;
@@ -646,7 +656,9 @@ void launch(AdjustArgs a, hipStream_t st) {
 // 52.0 against 56.1 us at B=128, R=17, V=32000 and 165 against 174 us at
 // V=128256 (bf16, penalties and masks).  Where rows start off a 16-byte
 // boundary every tile's ends share cache lines with its neighbours', and two
-// vectors have half as many ends: 209 against 221 us at V=128255.
+// vectors have half as many ends: 186 against 202 us for 9 rows of 256 sessions,
+// V=128255, in bf16 with every rule, 47 against 54 for one row; in binary32,
+// though its kernel has 3 to 4 waves a SIMD, 361 against 379 and 64 against 71.
 template <typename T>
 void launch(const AdjustArgs& a, hipStream_t st) {
   constexpr int E = Lanes<T>::kE;

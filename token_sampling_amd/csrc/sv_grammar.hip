@@ -180,10 +180,13 @@ __device__ inline Token token_of(const sv_vocab& v, int id) {
 // their bit in the wave's words in LDS, which then go out whole.  Waves take
 // states as they become free, since some (inside a string) allow most tokens.
 //
-// 1500 states of an automaton of 1474 by 37, V=128256: 66 us, bound by issue
-// (218 vector, 94 scalar and 50 LDS instructions a state and tile), 24 MB
-// written.  20 states, V=32000: 12.6 us, the table's and the tokens' loads and
-// one state that allows most of a tile.  Steps: a lane for each token and state,
+// 1500 states of an automaton of 1474 by 37, V=128256: 65 us, 24 MB written.
+// Vector instructions issue in half of the time (218 of them, 94 scalar and 50
+// LDS instructions a state and tile); the waves, 4 on a SIMD, wait in 54% of
+// their cycles, by the code mostly for LDS lookups one after another.  With the
+// table in global memory (1799 to 7322 states by 37) 97 us.  20 states, V=32000:
+// 12.6 us, the table's and the tokens' loads and one state that allows most of a
+// tile.  Steps: a lane for each token and state,
 // the table in global memory, 803 us; in LDS, four states abreast, 309; tokens by
 // first column within 1024, a wave's states tested together, 186; this order with
 // a test of each token's length in each step, 115; the end() column instead, 66.
@@ -396,7 +399,8 @@ __global__ __launch_bounds__(kThreads) void k_masks(GrammarArgs a, const int32_t
 // A session's tokens: a wave holds 64 of them, one a lane, and walks them one
 // after another, every lane alike; the chain of lookups is what it waits for.
 // 8 drafts of 256 sessions: 8.6 us, of which 4 to bring a table of 109 KB to
-// LDS; 64 drafts of 1024 sessions, up to 400 bytes each: 18.8 us.  One lane a
+// LDS; 64 drafts of 1024 sessions, up to 400 bytes each: 18.7 us.  Automata that
+// do not fit take 7.3 and 28 us (nothing to bring, lookups slower).  One lane a
 // session with the table in global memory took 16 and 103 us.
 template <int kEntries>
 __global__ __launch_bounds__(kThreads) void k_walk(GrammarArgs a, const int32_t* states,

@@ -3,9 +3,13 @@
 //
 // A token is an add on its count and an or on its bit; whole numbers, so the
 // order of the atomics does not matter.  The committed tokens of 256 sessions
-// take 2.4 us, a launch and four dependent loads.  64 prompts of up to 32768
-// tokens, V=128256, take 13 us: 7.6 to empty their slots (35 MB written, 4.6
-// TB/s), 5 to note 1e6 tokens.
+// take 2.3 us in a graph, a launch and four dependent loads.  64 prompts of up to
+// 32768 tokens, V=128256, take 13 us: 7.6 to empty their slots (35 MB written,
+// 4.6 TB/s), 5 to note 1e6 tokens.  The kernel and its workgroups go by the mean
+// length, so a line with one long session among short ones is slow: 102400
+// tokens of 256 sessions take 5.9 us in equal parts (prompts; outputs 9.7) and
+// 110 (147) where one session has 100000 of them, which fits two workgroups of
+// k_count_few; a call of its own takes it in 3.8 (8.8).
 #include "sv_common.hpp"
 
 namespace sv {
