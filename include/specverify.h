@@ -446,8 +446,9 @@ typedef struct sv_masks {
  * rounded once to dtype; tokens that no rule changes keep their bits.  The
  * quotient is the product with the rounded 1 / repetition, and the penalties and
  * bias(v) are summed before they meet z (an overflow of that sum is z's too):
- * before it is rounded to dtype, z is off by at most 3 * 2^-24 of the sum of the
- * magnitudes of its quotient or product, frequency * c, presence and bias(v).
+ * before it is rounded to dtype, z is off by three roundings of 2^-24 at most,
+ * relative to the sum of the magnitudes of its quotient or product, frequency *
+ * c, presence and bias(v) (for counts up to 2^24, which binary32 holds).
  * Rows a session does not use are neither read nor written.  A mask that allows
  * nothing leaves a row of -inf, which the acceptance step reports as
  * SV_S_BAD_LOGITS.
