@@ -100,6 +100,7 @@ typedef struct sv_sdcp_session {
  * p_tok holds p_i(x_i) at every position and q_tok is -1. */
 enum { SV_RULE_GREEDY = 1, SV_RULE_SPECULATIVE = 2, SV_RULE_RELAXED = 192 };
 enum { SV_BF16 = 0, SV_FP32 = 1 };                   /* logits element type */
+enum { SV_FP16 = 2 };                                /* caches only, beside SV_BF16 */
 
 /* Call-level return codes of sv_verify, sv_verify_sdcp and sv_verify_qrows. */
 enum {
@@ -119,7 +120,9 @@ enum {
   SV_S_BAD_PROPOSAL = -1,  /* a token outside [0, V); or, after the logits check,
                               q_i(x_i) == 0 for some i <= m[b] (sdcp-bad-proposal) */
   SV_S_BAD_LOGITS = -5,    /* NaN / +inf, or no finite logit, in a row the rule reads */
-  SV_S_BAD_CONTROL = -6    /* sv_adjust_logits only: penalties, slot, bias or mask out of range */
+  SV_S_BAD_CONTROL = -6,   /* sv_adjust_logits only: penalties, slot, bias or mask out of range */
+  SV_S_NO_PAGES = -7,      /* sv_cache_reserve only: not enough free pages */
+  SV_S_BAD_CACHE = -8      /* sv_cache_*: slot out of range, listed twice, or pages missing */
 };
 
 /* Bytes of device workspace sv_verify needs for (B, M, V).  0 if the sizes
@@ -552,6 +555,163 @@ int sv_grammar_masks(const sv_grammar *grammar, const sv_vocab *vocab, const int
 int sv_grammar_advance(const sv_grammar *grammar, const sv_vocab *vocab, const int32_t *states,
                        const int32_t *tokens, const int32_t *lens, int32_t B, int32_t L,
                        int32_t *out_states, int32_t *last, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The target model's cache of keys and values, in pages, and the attention that
+ * reads it (textbook chapter, sections on the KV cache, on pages with copy on
+ * write and on prefix caching).  A verifying round of B sessions:
+ *   sv_cache_reserve    pages for the round's rows
+ *   sv_cache_plan       how the round's attention is split, once for all layers
+ *   per layer: sv_cache_write, then sv_cache_attention
+ *   sv_verify_commit    on the logits
+ *   sv_cache_keep       the committed tokens kept (count = emitted_len), the
+ *                       pages behind them freed
+ * Row 0 of a round is the last committed token, whose keys are not cached yet,
+ * rows 1..M are the drafted ones: of these M + 1 rows the emitted_len first ones
+ * stay.  Everything stays on the device; every call only enqueues work on
+ * stream, allocates nothing and keeps no pointer; the host structs are read
+ * before it returns.  Calls that overlap on the same cache race, except that
+ * attention and plans only read it.
+ * ------------------------------------------------------------------------- */
+#define SV_CACHE_B_MAX 4096          /* most sessions per call */
+#define SV_CACHE_SLOTS_MAX (1 << 16) /* most slots of a cache */
+#define SV_CACHE_PAGES_MAX (1 << 20) /* most pages, in all and of a session */
+
+/* A pool of n_pages pages of `page` tokens in each of n_layers layers, and n_slots
+ * slots, each with one session's list of pages (a HOST struct of DEVICE
+ * pointers).  Slot h holds lens[h] tokens; its pages are table[h][0] ..
+ * table[h][held[h] - 1], token t in page t / page; entries behind are -1.
+ * refs[p] is how many lists hold page p, 0: the page is free.  Pages that
+ * several lists hold are never written.  An empty cache has table = -1 and
+ * lens = held = refs = 0; afterwards the calls below keep all four.
+ * k and v are [n_layers, n_pages, n_kv, page, head_dim] of dtype; the page *
+ * head_dim elements of a head stand in the order in which the matrix
+ * instructions read them: with token t = ((T * 4 + a) * 2 + b) * 4 + c and
+ * dimension d = (C * 4 + g) * 8 + e (a, c, g < 4, b < 2, e < 8), keys are laid out
+ * as [T][b][C][g][a][c][e]; with t = (T * 4 + g) * 8 + e and d = n * 16 + m (g < 4,
+ * e < 8, m < 16), values as [T][n][g][m][e].  16-byte aligned.
+ *   dtype SV_BF16 or SV_FP16; page 32, 64, 128 or 256; head_dim 64, 96, 128 or
+ *   256; 1 <= n_slots <= SV_CACHE_SLOTS_MAX; 1 <= n_pages, max_pages <=
+ *   SV_CACHE_PAGES_MAX; 1 <= n_kv <= 1024; 1 <= n_layers <= 4096. */
+typedef struct sv_cache {
+  void *k, *v;
+  int32_t *table; /* [n_slots, max_pages] */
+  int32_t *lens;  /* [n_slots] */
+  int32_t *held;  /* [n_slots] */
+  int32_t *refs;  /* [n_pages] */
+  int32_t dtype, n_layers, n_pages, n_kv, page, head_dim, n_slots, max_pages;
+} sv_cache;
+
+/* Common to the calls below: slots [B] int32 (or NULL: slot b), -1 for a place
+ * that no session has, which is left alone (status 0); a slot outside
+ * [-1, n_slots), or listed twice by a call that changes the cache, fails its
+ * sessions with SV_S_BAD_CACHE, all places that list it.  A failed session's
+ * slot, pages and lengths stay as they were.  status [B] int32 or NULL: 0 or
+ * SV_S_*.  1 <= B <= SV_CACHE_B_MAX.  Return codes: SV_OK, SV_ERR_ARG,
+ * SV_ERR_WORKSPACE or SV_ERR_DEVICE. */
+
+/* Bytes of device workspace for sv_cache_reserve, sv_cache_compact (contents
+ * need not be initialised; calls that overlap need distinct ones).  0 if the
+ * sizes are out of range. */
+size_t sv_cache_workspace_bytes(const sv_cache *cache, int32_t B);
+
+/*
+ * Pages for add[b] more tokens of each session.  Pages are taken in the order of
+ * the sessions, lowest free page first.  Where the next token falls into a
+ * page that other lists hold too, the session first gets a copy of it (of the
+ * blocks of 32 tokens in use, in every layer) in place of it.  A session is
+ * served if the pages that it and the sessions before it want (those that fail
+ * otherwise want none) are there, else it fails with SV_S_NO_PAGES; one that
+ * wants none is always served.  SV_S_LIMIT: add[b] < 0, or more than max_pages
+ * pages in all.  Lengths stay.
+ */
+int sv_cache_reserve(const sv_cache *cache, const int32_t *slots, const int32_t *add, int32_t B,
+                     int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The session's length becomes count[b] (absolute != 0) or lens + count[b], and
+ * its pages behind that length are let go (free where no other list holds them).
+ * SV_S_LIMIT: count[b] < 0, or a length beyond the session's pages.  count = 0,
+ * absolute: the slot is emptied.
+ */
+int sv_cache_keep(const sv_cache *cache, const int32_t *slots, const int32_t *count, int32_t absolute,
+                  int32_t B, int32_t *status, void *stream);
+
+/*
+ * Slot dst[i] takes over the tokens of slot src[i]: its list of pages as far as its
+ * length reaches, without a copy.  dst must be empty (held = 0), be listed once
+ * and not be a src of the call: SV_S_BAD_CACHE.  Several dst may have one src.  A
+ * place with src or dst of -1 is left alone.
+ */
+int sv_cache_fork(const sv_cache *cache, const int32_t *src, const int32_t *dst, int32_t n,
+                  int32_t *status, void *stream);
+
+/*
+ * Moves the pages in use to the pool's front: with U pages in use, the i-th used
+ * page at or behind U goes to the i-th free page before U, in every layer, and
+ * the lists follow.  used [1] int32: U.  moved [n_pages] int32 or NULL: where each
+ * page went (its own number if it stayed, -1 for a page that was free).
+ */
+int sv_cache_compact(const sv_cache *cache, int32_t *used, int32_t *moved, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Writes rows of keys and values into the pages of a layer.  Row i of session b
+ * goes to position lens + i (lengths stay, see sv_cache_keep).  Rows: k, v
+ * [B, R, n_kv, head_dim] of the cache's dtype at element strides of_session,
+ * of_row, of_head (>= 0, multiples of 8; dimensions contiguous, 16-byte aligned),
+ * of which session b has rows[b] (NULL: R; cut to [0, R]); or, with offsets (DEVICE
+ * [B + 1], ascending; rows must be NULL and R = all rows), [R, n_kv, head_dim],
+ * session b's rows being offsets[b] .. offsets[b + 1] - 1 (cut to [0, R)).  Rows
+ * that fall behind the session's pages, or into a page that other lists hold
+ * too, are skipped: a session that sv_cache_reserve did not serve changes no
+ * other.  A slot may not be listed twice.  Nothing else of a page changes.
+ */
+typedef struct sv_rows {
+  const void *k, *v;
+  int64_t k_session, k_row, k_head, v_session, v_row, v_head; /* strides */
+} sv_rows;
+int sv_cache_write(const sv_cache *cache, int32_t layer, const sv_rows *from, const int32_t *slots,
+                   const int32_t *rows, const int32_t *offsets, int32_t B, int32_t R, void *stream);
+
+/*
+ * The plan of a round's attention: which keys and rows go together.  Where
+ * neighbouring sessions (places without one between them do not count) have
+ * the same leading pages, these are read once for all of them, on up to two
+ * levels: what a run of sessions shares, and what parts of the run share
+ * beyond it; so sessions that share should be listed side by side.  The result
+ * depends on it by the order of its sums alone.  rows [B] int32 (NULL: R): the
+ * session's rows of the round.  n_heads: query heads, a multiple of n_kv.
+ * plan: DEVICE, sv_cache_plan_bytes(); it holds for every layer as long as lists,
+ * lengths, slots and rows stay as they are.  status: SV_S_BAD_CACHE also where the
+ * rows' positions lens .. lens + rows - 1 are not all in pages that the session
+ * alone holds (sv_cache_reserve did not serve it); SV_S_LIMIT: rows[b] outside
+ * [0, R].  1 <= R <= SV_M_MAX + 1, n_heads <= 1024.
+ */
+size_t sv_cache_plan_bytes(const sv_cache *cache, int32_t n_heads, int32_t B, int32_t R);
+int sv_cache_plan(const sv_cache *cache, const int32_t *slots, const int32_t *rows, int32_t n_heads,
+                  int32_t B, int32_t R, int32_t *status, void *plan, size_t plan_bytes, void *stream);
+
+/*
+ * Attention of a round's rows over a layer of the cache:
+ *   out[b][r][h] = sum_t w_t v_t,  w = softmax over t of scale * q[b][r][h] . k_t,
+ * t = 0 .. lens + r, keys and values of head h / (n_heads / n_kv).  The rows' own
+ * keys and values must be written.  Scores, weights' sums and outputs are kept
+ * in binary32; a weight is rounded to dtype before it meets the values, as
+ * the matrix instructions take it (relative to the row's largest), and the
+ * output once.  What a row does not see has no part in it, NaN and infinities
+ * included.  q [B, R, n_heads, head_dim] of dtype at element strides q_session,
+ * q_row, q_head (>= 0, multiples of 8; 16-byte aligned); out the same shape,
+ * contiguous, not overlapping q.  Rows that a session does not use are neither read nor
+ * written; all R rows of a failed session become NaN.  scale > 0, finite.
+ * plan: of sv_cache_plan with the same cache, n_heads, B and R.  workspace:
+ * sv_cache_attention_bytes(); calls that overlap need distinct ones.
+ */
+size_t sv_cache_attention_bytes(const sv_cache *cache, int32_t n_heads, int32_t B, int32_t R);
+int sv_cache_attention(const sv_cache *cache, int32_t layer, const void *q, int64_t q_session,
+                       int64_t q_row, int64_t q_head, float scale, const void *plan,
+                       int32_t n_heads, int32_t B, int32_t R, void *out, void *workspace,
+                       size_t workspace_bytes, void *stream);
 
 /* Benchmark hook, not part of the acceptance step: hipEvent_t handles that
  * the sv_verify* calls made afterwards from the calling host thread record on

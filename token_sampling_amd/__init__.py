@@ -26,6 +26,7 @@ LIB_PATH = os.path.join(_HERE, "libspecverify.so")
 
 BF16 = 0
 FP32 = 1
+FP16 = 2  # caches only
 RULE_GREEDY = 1
 RULE_SPECULATIVE = 2
 RULE_RELAXED = 192  # private use: accept while p_i(x_i) > 0
@@ -39,6 +40,8 @@ S_Q_UNAVAILABLE = -3
 S_BAD_PROFILE = -4
 S_BAD_LOGITS = -5
 S_BAD_CONTROL = -6  # adjust_logits: penalties, slot, bias offsets or mask row out of range
+S_NO_PAGES = -7  # cache_reserve: not enough free pages
+S_BAD_CACHE = -8  # cache_*: slot out of range, listed twice, or pages missing
 
 SAMPLING_DTYPE = np.dtype(
     [("temperature_milli", "<u4"), ("top_k", "<u4"), ("top_p_milli", "<u4"),
@@ -68,7 +71,10 @@ EXPORTED = ("sv_workspace_bytes", "sv_verify", "sv_verify_sdcp", "sv_verify_qrow
             "sv_verify_early", "sv_commit",
             "sv_prefix_digest", "sv_contract_digest", "sv_strerror", "sv_status_str",
             "sv_version", "sv_bench_row_events", "sv_verify_noalloc", "sv_verify_commit",
-            "sv_adjust_logits", "sv_count_tokens", "sv_grammar_masks", "sv_grammar_advance")
+            "sv_adjust_logits", "sv_count_tokens", "sv_grammar_masks", "sv_grammar_advance",
+            "sv_cache_workspace_bytes", "sv_cache_reserve", "sv_cache_keep", "sv_cache_fork",
+            "sv_cache_compact", "sv_cache_write", "sv_cache_plan_bytes", "sv_cache_plan",
+            "sv_cache_attention_bytes", "sv_cache_attention")
 # Per-session penalties for repeated tokens (sv_penalties, 16 bytes).
 PENALTIES_DTYPE = np.dtype([("repetition", "<f4"), ("frequency", "<f4"), ("presence", "<f4"),
                             ("reserved", "<u4")], align=True)
@@ -112,6 +118,17 @@ class _Vocab(ctypes.Structure):
                 ("n_bytes", ctypes.c_int32), ("n_end", ctypes.c_int32), ("V", ctypes.c_int32)]
 
 
+class _Cache(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("k", "v", "table", "lens", "held", "refs")] + [
+        (f, ctypes.c_int32) for f in ("dtype", "n_layers", "n_pages", "n_kv", "page", "head_dim",
+                                      "n_slots", "max_pages")]
+
+
+class _Rows(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (f, ctypes.c_int64) for f in ("k_session", "k_row", "k_head", "v_session", "v_row", "v_head")]
+
+
 class History(NamedTuple):
     """Which tokens each slot has had (sv_history): counts [n_slots, V] int32 of
     the output tokens, seen [n_slots, 2, W] int32 bit rows over the vocabulary, W
@@ -143,6 +160,30 @@ class Vocab(NamedTuple):
     bytes: "torch.Tensor"  # noqa: F821
     offsets: "torch.Tensor"  # noqa: F821
     end: "torch.Tensor"  # noqa: F821
+
+
+class Cache(NamedTuple):
+    """A paged cache of keys and values (sv_cache): k, v [n_layers, n_pages, n_kv,
+    page, head_dim] bf16/fp16, whose page * head_dim elements of a head stand in the
+    matrix instructions' order (cache_order); table [n_slots, max_pages] the slots'
+    pages (-1: none), lens and held [n_slots] their tokens and pages, refs [n_pages]
+    how many lists hold each page, all int32.  See make_cache."""
+    k: "torch.Tensor"  # noqa: F821
+    v: "torch.Tensor"  # noqa: F821
+    table: "torch.Tensor"  # noqa: F821
+    lens: "torch.Tensor"  # noqa: F821
+    held: "torch.Tensor"  # noqa: F821
+    refs: "torch.Tensor"  # noqa: F821
+
+
+class CachePlan(NamedTuple):
+    """How a round's attention is split (cache_plan), for B sessions of up to R rows
+    and n_heads query heads; status [B] int32."""
+    buffer: "torch.Tensor"  # noqa: F821
+    status: "torch.Tensor"  # noqa: F821
+    n_heads: int
+    B: int
+    R: int
 
 
 class HipEvent:
@@ -262,8 +303,23 @@ def lib():
         L.sv_grammar_masks.argtypes = [ctypes.POINTER(_Grammar), ctypes.POINTER(_Vocab), p, i, p, p]
         L.sv_grammar_advance.argtypes = [ctypes.POINTER(_Grammar), ctypes.POINTER(_Vocab), p, p, p,
                                          i, i, p, p, p]
-        for f in (L.sv_adjust_logits, L.sv_count_tokens, L.sv_grammar_masks, L.sv_grammar_advance):
+        n, c = ctypes.c_size_t, ctypes.POINTER(_Cache)
+        L.sv_cache_reserve.argtypes = [c, p, p, i, p, p, n, p]
+        L.sv_cache_keep.argtypes = [c, p, p, i, i, p, p]
+        L.sv_cache_fork.argtypes = [c, p, p, i, p, p]
+        L.sv_cache_compact.argtypes = [c, p, p, p, n, p]
+        L.sv_cache_write.argtypes = [c, i, ctypes.POINTER(_Rows), p, p, p, i, i, p]
+        L.sv_cache_plan.argtypes = [c, p, p, i, i, i, p, p, n, p]
+        L.sv_cache_attention.argtypes = [c, i, p] + [ctypes.c_int64] * 3 + [
+            ctypes.c_float, p, i, i, i, p, p, n, p]
+        for f in (L.sv_adjust_logits, L.sv_count_tokens, L.sv_grammar_masks, L.sv_grammar_advance,
+                  L.sv_cache_reserve, L.sv_cache_keep, L.sv_cache_fork, L.sv_cache_compact,
+                  L.sv_cache_write, L.sv_cache_plan, L.sv_cache_attention):
             f.restype = ctypes.c_int
+        L.sv_cache_workspace_bytes.argtypes = [c, i]
+        L.sv_cache_plan_bytes.argtypes = L.sv_cache_attention_bytes.argtypes = [c, i, i, i]
+        for f in (L.sv_cache_workspace_bytes, L.sv_cache_plan_bytes, L.sv_cache_attention_bytes):
+            f.restype = n
         _lib = L
     return _lib
 
@@ -942,4 +998,317 @@ def grammar_advance(grammar, vocab, states, tokens, lens=None, out=None, stream=
                                       out["states"].data_ptr(), out["last"].data_ptr(), handle)
     if rc != OK:
         raise SvError(f"sv_grammar_advance failed: {strerror(rc)} ({rc})")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# The paged cache of keys and values and the attention that reads it (sv_cache_*).
+
+def make_cache(n_slots, n_pages, max_pages, n_kv, head_dim, n_layers=1, page=64, dtype=None,
+               device="cuda"):
+    """An empty Cache: n_pages pages of `page` tokens (32, 64, 128 or 256) in each
+    layer, n_slots sessions of at most max_pages pages.  head_dim 64, 96, 128 or 256;
+    dtype torch.bfloat16 (None) or torch.float16."""
+    import torch
+
+    dtype = torch.bfloat16 if dtype is None else dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("caches are bfloat16 or float16")
+    if page not in (32, 64, 128, 256):
+        raise ValueError("page must be 32, 64, 128 or 256")
+    if head_dim not in (64, 96, 128, 256):
+        raise ValueError("head_dim must be 64, 96, 128 or 256")
+    shape = (n_layers, n_pages, n_kv, page, head_dim)
+
+    def ints(value, *size):
+        return torch.full(size, value, dtype=torch.int32, device=device)
+
+    return Cache(torch.empty(shape, dtype=dtype, device=device),
+                 torch.empty(shape, dtype=dtype, device=device), ints(-1, n_slots, max_pages),
+                 ints(0, n_slots), ints(0, n_slots), ints(0, n_pages))
+
+
+def cache_order(page, head_dim):
+    """Where token t's dimension d of a head stands among the page * head_dim elements
+    of a page: two [page, head_dim] int64 arrays, for keys and for values.  With
+    them k[layer, p, head].flatten()[keys] are the page's keys by token."""
+    place = np.arange(page * head_dim)
+    keys = place.reshape(page // 32, 2, head_dim // 32, 4, 4, 4, 8).transpose(0, 4, 1, 5, 2, 3, 6)
+    values = place.reshape(page // 32, head_dim // 16, 4, 16, 8).transpose(0, 2, 4, 1, 3)
+    return keys.reshape(page, head_dim), values.reshape(page, head_dim)
+
+
+def _cache_struct(cache, dev):
+    import torch
+
+    if cache.k.dtype is torch.bfloat16:
+        dt = BF16
+    elif cache.k.dtype is torch.float16:
+        dt = FP16
+    else:
+        raise TypeError("caches are bfloat16 or float16")
+    if cache.k.dim() != 5 or cache.table.dim() != 2:
+        raise ValueError("cache.k must be [n_layers, n_pages, n_kv, page, head_dim], cache.table "
+                         "[n_slots, max_pages]")
+    shape = cache.k.shape
+    n_layers, n_pages, n_kv, page, head_dim = shape
+    n_slots, max_pages = cache.table.shape
+    return _Cache(_want(cache.k, "cache.k", cache.k.dtype, shape, dev),
+                  _want(cache.v, "cache.v", cache.k.dtype, shape, dev),
+                  _want(cache.table, "cache.table", torch.int32, (n_slots, max_pages), dev),
+                  _want(cache.lens, "cache.lens", torch.int32, (n_slots,), dev),
+                  _want(cache.held, "cache.held", torch.int32, (n_slots,), dev),
+                  _want(cache.refs, "cache.refs", torch.int32, (n_pages,), dev),
+                  dt, n_layers, n_pages, n_kv, page, head_dim, n_slots, max_pages)
+
+
+def _cache_slots(cache, slots, B, dev):
+    import torch
+
+    if slots is not None:
+        return _want(slots, "slots", torch.int32, (B,), dev)
+    if cache.table.shape[0] < B:
+        raise ValueError("the cache has fewer slots than sessions")
+    return None
+
+
+def _status(status, B, dev):
+    import torch
+
+    if status is None:
+        return torch.empty(B, dtype=torch.int32, device=dev)
+    _want(status, "status", torch.int32, (B,), dev)
+    return status
+
+
+def _bytes(workspace, need, name, dev):
+    """A workspace of at least need bytes (need 0: sizes that the library refuses)."""
+    import torch
+
+    if need == 0:
+        raise SvError("sizes out of range")
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
+    _check(workspace, name, None, None, dev)
+    have = workspace.numel() * workspace.element_size()
+    if have < need:
+        raise SvError(f"{name} too small")
+    return workspace, have
+
+
+def _raise(rc, name):
+    if rc != OK:
+        raise SvError(f"{name} failed: {strerror(rc)} ({rc})")
+
+
+def cache_reserve(cache, add, slots=None, status=None, workspace=None, stream=None):
+    """sv_cache_reserve: pages for add [B] int32 more tokens of the sessions on slots
+    [B] int32 (None: slot b; -1: none), and a copy of the page that the next token
+    falls into where other lists hold it too.  Returns status [B] int32: 0,
+    S_NO_PAGES, S_LIMIT or S_BAD_CACHE."""
+    import torch
+
+    dev = _device_of(add, "add")
+    c = _cache_struct(cache, dev)
+    B = add.numel()
+    p_add = _want(add, "add", torch.int32, (B,), dev)
+    p_slots = _cache_slots(cache, slots, B, dev)
+    handle, on = _launch(dev, stream)
+    with on:
+        status = _status(status, B, dev)
+        need = lib().sv_cache_workspace_bytes(ctypes.byref(c), B)
+        workspace, size = _bytes(workspace, need, "workspace", dev)
+        rc = lib().sv_cache_reserve(ctypes.byref(c), p_slots, p_add, B, status.data_ptr(),
+                                    workspace.data_ptr(), size, handle)
+    _raise(rc, "sv_cache_reserve")
+    return status
+
+
+def cache_keep(cache, count, slots=None, absolute=False, status=None, stream=None):
+    """sv_cache_keep: the sessions' lengths become lens + count [B] int32 (the
+    emitted_len of a commit), or count itself (absolute), and the pages behind are
+    let go.  Returns status [B] int32: 0, S_LIMIT or S_BAD_CACHE."""
+    import torch
+
+    dev = _device_of(count, "count")
+    c = _cache_struct(cache, dev)
+    B = count.numel()
+    p_count = _want(count, "count", torch.int32, (B,), dev)
+    p_slots = _cache_slots(cache, slots, B, dev)
+    handle, on = _launch(dev, stream)
+    with on:
+        status = _status(status, B, dev)
+        rc = lib().sv_cache_keep(ctypes.byref(c), p_slots, p_count, int(absolute), B,
+                                 status.data_ptr(), handle)
+    _raise(rc, "sv_cache_keep")
+    return status
+
+
+def cache_fork(cache, src, dst, status=None, stream=None):
+    """sv_cache_fork: slot dst[i] (empty) takes over the tokens of slot src[i], [n]
+    int32 each (-1: none), sharing its pages.  Returns status [n] int32: 0 or
+    S_BAD_CACHE."""
+    import torch
+
+    dev = _device_of(src, "src")
+    c = _cache_struct(cache, dev)
+    n = src.numel()
+    p_src = _want(src, "src", torch.int32, (n,), dev)
+    p_dst = _want(dst, "dst", torch.int32, (n,), dev)
+    handle, on = _launch(dev, stream)
+    with on:
+        status = _status(status, n, dev)
+        rc = lib().sv_cache_fork(ctypes.byref(c), p_src, p_dst, n, status.data_ptr(), handle)
+    _raise(rc, "sv_cache_fork")
+    return status
+
+
+def cache_compact(cache, used=None, moved=None, workspace=None, stream=None):
+    """sv_cache_compact: moves the pages in use to the pool's front, the lists with
+    them.  Returns used [1] int32, the pages in use.  moved: None, or [n_pages] int32
+    for where each page went (-1: it was free)."""
+    import torch
+
+    dev = _device_of(cache.k, "cache.k")
+    c = _cache_struct(cache, dev)
+    p_moved = None if moved is None else _want(moved, "moved", torch.int32, (c.n_pages,), dev)
+    handle, on = _launch(dev, stream)
+    with on:
+        if used is None:
+            used = torch.empty(1, dtype=torch.int32, device=dev)
+        else:
+            _want(used, "used", torch.int32, (1,), dev)
+        need = lib().sv_cache_workspace_bytes(ctypes.byref(c), 1)
+        workspace, size = _bytes(workspace, need, "workspace", dev)
+        rc = lib().sv_cache_compact(ctypes.byref(c), used.data_ptr(), p_moved,
+                                    workspace.data_ptr(), size, handle)
+    _raise(rc, "sv_cache_compact")
+    return used
+
+
+def _row_strides(t, name, shape, dtype, dev):
+    """A tensor's address and strides, its last axis contiguous; strides of axes of one
+    place do not count."""
+    import torch
+
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    strides = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+    if t.numel() == 0:
+        return None, [0] * (t.dim() - 1)
+    if strides[-1] != 1:
+        raise ValueError(f"the last axis of {name} must be contiguous")
+    if any(s % 8 for s in strides[:-1]) or t.data_ptr() % 16:
+        raise ValueError(f"rows of {name} must begin at multiples of 16 bytes")
+    return t.data_ptr(), strides[:-1]
+
+
+def cache_write(cache, layer, k, v, slots=None, rows=None, offsets=None, stream=None):
+    """sv_cache_write: rows of keys and values into the pages of a layer, from position
+    lens on (lengths stay, see cache_keep).  k, v [B, R, n_kv, head_dim] (slices of a
+    wider projection will do), of which session b has rows[b] (None: R); or, with
+    offsets [B + 1] int32, [N, n_kv, head_dim], session b's being offsets[b] ..
+    offsets[b + 1] - 1.  Rows without pages that the session alone holds are
+    skipped (cache_reserve's status tells)."""
+    import torch
+
+    dev = _device_of(k, "k")
+    c = _cache_struct(cache, dev)
+    p_rows = p_offsets = None
+    if offsets is not None:
+        if rows is not None:
+            raise ValueError("give rows or offsets, not both")
+        if k.dim() != 3:
+            raise ValueError("k must be [N, n_kv, head_dim] with offsets")
+        B, R = offsets.numel() - 1, _int32(k.shape[0], "k")
+        p_offsets = _want(offsets, "offsets", torch.int32, (B + 1,), dev)
+        shape = (R, c.n_kv, c.head_dim)
+    else:
+        if k.dim() != 4:
+            raise ValueError("k must be [B, R, n_kv, head_dim] (or one line, with offsets)")
+        B, R = k.shape[:2]
+        shape = (B, R, c.n_kv, c.head_dim)
+        if rows is not None:
+            p_rows = _want(rows, "rows", torch.int32, (B,), dev)
+    p_k, k_strides = _row_strides(k, "k", shape, cache.k.dtype, dev)
+    p_v, v_strides = _row_strides(v, "v", shape, cache.k.dtype, dev)
+    if offsets is not None:
+        k_strides, v_strides = [0] + k_strides, [0] + v_strides
+    p_slots = _cache_slots(cache, slots, B, dev)
+    handle, on = _launch(dev, stream)
+    with on:
+        rc = lib().sv_cache_write(ctypes.byref(c), layer,
+                                  ctypes.byref(_Rows(p_k, p_v, *k_strides, *v_strides)), p_slots,
+                                  p_rows, p_offsets, B, R, handle)
+    _raise(rc, "sv_cache_write")
+
+
+def cache_plan(cache, n_heads, R, rows=None, slots=None, B=None, out=None, stream=None):
+    """sv_cache_plan: how the attention of a round of up to R rows a session is split,
+    for all layers, as long as the cache's lists and lengths, slots [B] int32 (None:
+    slot b) and rows [B] int32 (None: R; B then tells how many) stay as they are.  Keys
+    that neighbouring sessions share are read once for all of them.  out: a CachePlan
+    of the same sizes to write again."""
+    import torch
+
+    dev = _device_of(cache.k, "cache.k")
+    c = _cache_struct(cache, dev)
+    given = rows if rows is not None else slots
+    if given is not None:
+        if B is not None and B != given.numel():
+            raise ValueError("B does not go with rows or slots")
+        B = given.numel()
+    elif B is None:
+        B = c.n_slots
+    p_rows = None if rows is None else _want(rows, "rows", torch.int32, (B,), dev)
+    p_slots = _cache_slots(cache, slots, B, dev)
+    need = lib().sv_cache_plan_bytes(ctypes.byref(c), n_heads, B, R)
+    handle, on = _launch(dev, stream)
+    with on:
+        if out is not None and (out.n_heads, out.B, out.R) != (n_heads, B, R):
+            raise ValueError("out is a plan of other sizes")
+        buffer, size = _bytes(None if out is None else out.buffer, need, "out.buffer", dev)
+        status = _status(None if out is None else out.status, B, dev)
+        rc = lib().sv_cache_plan(ctypes.byref(c), p_slots, p_rows, n_heads, B, R, status.data_ptr(),
+                                 buffer.data_ptr(), size, handle)
+    _raise(rc, "sv_cache_plan")
+    return CachePlan(buffer, status, n_heads, B, R)
+
+
+def cache_attention(cache, layer, q, plan, scale=None, out=None, workspace=None, stream=None):
+    """sv_cache_attention: attention of a round's rows q [B, R, n_heads, head_dim] (a
+    slice of a wider projection will do) over a layer of the cache, row r of a session
+    over positions 0 .. lens + r; its own keys and values must be written.  scale:
+    None for 1 / sqrt(head_dim).  out: None for a new tensor, or one like it.  Rows
+    that a session does not use are not written, rows of a failed session become NaN."""
+    import torch
+
+    dev = _device_of(q, "q")
+    c = _cache_struct(cache, dev)
+    B, R, n_heads = plan.B, plan.R, plan.n_heads
+    shape = (B, R, n_heads, c.head_dim)
+    p_q, strides = _row_strides(q, "q", shape, cache.k.dtype, dev)
+    scale = c.head_dim ** -0.5 if scale is None else float(scale)
+    need = lib().sv_cache_attention_bytes(ctypes.byref(c), n_heads, B, R)
+    _bytes(plan.buffer, lib().sv_cache_plan_bytes(ctypes.byref(c), n_heads, B, R), "plan", dev)
+    handle, on = _launch(dev, stream)
+    with on:
+        if out is None:
+            out = torch.empty(shape, dtype=q.dtype, device=dev)
+        else:
+            _want(out, "out", q.dtype, shape, dev)
+            hi = p_q + 2 * (sum(s * (n - 1) for s, n in zip(strides, shape)) + c.head_dim)
+            if out.data_ptr() < hi and p_q < out.data_ptr() + 2 * out.numel():
+                raise ValueError("out overlaps q")
+        workspace, size = _bytes(workspace, need, "workspace", dev)
+        rc = lib().sv_cache_attention(ctypes.byref(c), layer, p_q, *strides, scale,
+                                      plan.buffer.data_ptr(), n_heads, B, R, out.data_ptr(),
+                                      workspace.data_ptr(), size, handle)
+    _raise(rc, "sv_cache_attention")
     return out

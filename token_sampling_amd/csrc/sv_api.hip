@@ -329,6 +329,8 @@ extern "C" const char* sv_status_str(int status) {
     case SV_S_BAD_PROFILE: return "bad profile: unknown rule, top_p_milli > 1000 or reserved != 0";
     case SV_S_BAD_LOGITS: return "bad logits: NaN or +inf, or no finite logit, in a row read";
     case SV_S_BAD_CONTROL: return "bad control: penalties, history slot, bias offsets or mask row out of range";
+    case SV_S_NO_PAGES: return "no pages: not enough free pages in the cache";
+    case SV_S_BAD_CACHE: return "bad cache slot: out of range, listed twice, in use, or without pages of its own for the rows";
     default: return "unknown status";
   }
 }
