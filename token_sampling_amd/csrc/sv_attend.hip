@@ -18,6 +18,7 @@ struct Bf {
   typedef __bf16 vec8 __attribute__((ext_vector_type(8)));
   typedef __bf16 vec2 __attribute__((ext_vector_type(2)));
   static constexpr uint32_t kExp = 0x7F80u;  // exponent of infinities and NaN
+  __device__ static inline float value(uint32_t bits) { return __uint_as_float(bits << 16); }
   __device__ static inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(vec8, a),
                                                    __builtin_bit_cast(vec8, b), c, 0, 0, 0);
@@ -27,6 +28,7 @@ struct Hf {
   typedef _Float16 vec8 __attribute__((ext_vector_type(8)));
   typedef _Float16 vec2 __attribute__((ext_vector_type(2)));
   static constexpr uint32_t kExp = 0x7C00u;
+  __device__ static inline float value(uint32_t bits) { return (float)__builtin_bit_cast(_Float16, (uint16_t)bits); }
   __device__ static inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vec8, a),
                                                   __builtin_bit_cast(vec8, b), c, 0, 0, 0);
@@ -43,279 +45,542 @@ struct AttendArgs {
   const char* q;
   int64_t q_session, q_row, q_head;
   char* out;
-  float* part_o;   // [slots][per][head_dim]
-  float* part_ml;  // [slots][per][2]
-  float scale;     // times log2 e
-  int64_t base;    // the layer's first element
-  int32_t G, B, R, per;
+  float* part_o[2];   // of the lines' partial results: [slots][rows][head_dim]
+  float* part_ml[2];  // [slots][rows][2]
+  int32_t rows[2];    // of a set at most
+  float scale;        // times log2 e
+  int64_t base;       // the layer's first element
+  int32_t G, B, R;
 };
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 
-// A workgroup goes over a piece of the line, set by set: its waves take the tiles of
-// 32 keys in turn, each for all rows of the set, and join at the set's end.
-template <typename E, int D, int NT>
-__global__ __launch_bounds__(kThreads) void k_attend(AttendArgs a) {
-  constexpr int kC = D / 32, kN = D / 16;
-  __shared__ f32x4 red[kWaves][kN][kWave];
-  __shared__ float red_m[kWaves][NT * 16], red_l[kWaves][NT * 16];
-  const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
-  const int col = lane % 16, g = lane / 16;
-  const CacheView& c = a.c;
-  const int64_t total = a.p.head->total, piece = a.p.head->piece;
-  int64_t x = blockIdx.x * piece;
-  const int64_t x_end = min(x + piece, total);
-  if (x >= x_end) return;
-  const int4 start = a.p.starts[blockIdx.x];
-  int s = start.x, head = start.y, blk = start.z;
-  while (x < x_end) {
-    const AttendSet set = a.p.sets[s];
-    const int nb = set.blocks();
-    const int cnt = (int)min((int64_t)(nb - blk), x_end - x);
-    // ---- the set's rows
-    u32x4 q[NT][kC];
-    int lim[NT];  // a row sees the keys before it
-    int64_t out_at[NT];
+// A set's row j: where its query and output stand (-1: no such row), and the keys
+// that it sees (those before lim).
+struct Row {
+  int64_t q, out;
+  int lim;
+};
+__device__ inline Row row_at(const AttendArgs& a, const AttendSet& set, int head, int j) {
+  if (j >= set.n) return Row{-1, -1, 0};
+  const int jj = set.j0 + j, row = a.p.row_of[set.t0 + jj / a.G];
+  const int b = row / a.R, r = row % a.R, hq = head * a.G + jj % a.G;
+  return Row{b * a.q_session + r * a.q_row + hq * a.q_head,
+             ((int64_t)row * (a.G * a.c.n_kv) + hq) * a.c.head_dim, set.base + r + 1};
+}
+
+// An accumulated value tile of a narrow or wide set goes out: as a partial result, or as
+// the result where it is whole.
+template <typename E>
+__device__ inline void put4(char* out, f32x4 x, float norm) {
+  uint2 y;
+  y.x = pack2<E>(x[0] * norm, x[1] * norm);
+  y.y = pack2<E>(x[2] * norm, x[3] * norm);
+  *(uint2*)out = y;
+}
+
+// Where a piece of a line goes on.
+struct Cursor {
+  int64_t x, end;
+  int s, head, blk, sets, piece;
+  __device__ int64_t part() const { return (int64_t)head * sets + s + piece; }
+};
+constexpr int kXcds = 8;
+__device__ inline bool begin(const AttendArgs& a, int line, Cursor& at) {
+  const int64_t total = a.p.head->total[line], piece = a.p.head->piece[line];
+  at.piece = blockIdx.x % kXcds * (kPieces / kXcds) + blockIdx.x / kXcds;
+  at.sets = a.p.head->sets[line];
+  at.x = at.piece * piece;
+  at.end = min(at.x + piece, total);
+  if (at.x >= at.end) return false;
+  const int4 start = a.p.starts[line][at.piece];
+  at.s = start.x, at.head = start.y, at.blk = start.z;
+  return true;
+}
+__device__ inline void advance(Cursor& at, int blocks) {
+  at.x += blocks;
+  at.blk = 0;
+  if (++at.s == at.sets) at.s = 0, ++at.head;
+}
+
+// Scores of 32 keys' keys against 16 rows, a lane its row's: keys 8 g .. 8 g + 7.
+template <typename E, int kC>
+__device__ inline void score(const u32x4 (&kf)[kC], const u32x4 (&q)[kC], f32x4& z) {
+  z = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kC; ++i) z = E::mfma(kf[i], q[i], z);
+}
+
+// Scores become weights: 2^(z * scale - m), with m a value near the row's largest
+// score so far.  m follows the largest only where a score exceeds it by kSlack,
+// which after the first tiles hardly happens: the lanes need not agree on a tile's
+// largest, and what is summed is seldom multiplied.  Weights reach 2^kSlack, which
+// costs no digits in binary32 or in either 16-bit type.
+constexpr float kSlack = 8.0f;
+constexpr float kLowest = -3.402823466e38f;  // m of a row that has seen nothing
+template <typename E, bool kEdge, int NT, int kN>
+__device__ inline void weigh(f32x4 (&z)[NT][2], u32x4 (&w)[NT], float scale, int key, const int (&lim)[NT],
+                             float (&m)[NT], float (&l)[NT], f32x4 (&o)[NT][kN]) {
+  float top[NT];
+  bool far = false;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (kEdge) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (key + e >= lim[t]) z[t][e / 4][e % 4] = -INFINITY;
+    }
+    top[t] = z[t][0][0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) top[t] = fmaxf(top[t], z[t][e / 4][e % 4]);
+    top[t] *= scale;
+    far |= top[t] > m[t] + kSlack;
+  }
+  if (__any(far)) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int j = t * 16 + col;
-      lim[t] = 0;
-      out_at[t] = -1;
-      int64_t at = -1;
-      if (j < set.n) {
-        const int jj = set.j0 + j, place = set.t0 + jj / a.G, row = a.p.row_of[place];
-        const int b = row / a.R, r = row % a.R, hq = head * a.G + jj % a.G;
-        at = b * a.q_session + r * a.q_row + hq * a.q_head;
-        lim[t] = set.base + r + 1;
-        out_at[t] = ((int64_t)row * (a.G * c.n_kv) + hq) * D;
-      }
+      float now = fmaxf(top[t], lane_xor<16>(top[t]));
+      now = fmaxf(m[t], fmaxf(now, lane_xor<32>(now)));
+      const float keep = __builtin_amdgcn_exp2f(m[t] - now);
+      m[t] = now;
+      l[t] *= keep;
 #pragma unroll
-      for (int i = 0; i < kC; ++i)
-        q[t][i] = at >= 0 ? *(const u32x4*)(a.q + 2 * (at + i * 32 + g * 8)) : u32x4{0, 0, 0, 0};
+      for (int i = 0; i < kN; ++i) o[t][i] *= keep;
     }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float p[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      p[e] = __builtin_amdgcn_exp2f(fmaf(z[t][e / 4][e % 4], scale, -m[t]));
+      l[t] += p[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[t][e] = pack2<E>(p[2 * e], p[2 * e + 1]);
+  }
+}
+
+// Values of 32 keys meet the weights, 16 dimensions at a time; values(i) has them.
+template <typename E, int NT, int kN, typename V>
+__device__ inline void mix(const V& values, const u32x4 (&w)[NT], f32x4 (&o)[NT][kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const u32x4 vf = values(i);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) o[t][i] = E::mfma(vf, w[t], o[t][i]);
+  }
+}
+// The same where some rows do not see all keys: what lies behind the last key (never
+// written for this session) counts as 0.  False, and nothing done, where a value is
+// not finite: times a weight of 0 it would reach rows that do not see it.
+template <typename E, int NT, int kN, typename V>
+__device__ inline bool mix_edge(const V& values, const u32x4 (&w)[NT], int key, int key1, f32x4 (&o)[NT][kN]) {
+  const int g = threadIdx.x % kWave / 16;
+  u32x4 there;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    there[e] = (key + g * 8 + 2 * e < key1 ? 0x0000FFFFu : 0u) | (key + g * 8 + 2 * e + 1 < key1 ? 0xFFFF0000u : 0u);
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const u32x4 vf = values(i) & there;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      odd |= (vf[e] & E::kExp) == E::kExp || (vf[e] >> 16 & E::kExp) == E::kExp;
+  }
+  if (__any(odd)) return false;
+  mix<E>([&](int i) { return values(i) & there; }, w, o);
+  return true;
+}
+// Then: key by key, for the rows that see it, out of the values' 16-bit elements.
+template <typename E, int NT, int kN>
+__device__ inline void mix_slowly(const uint16_t* values, const u32x4 (&w)[NT], int key, int key1,
+                                  const int (&lim)[NT], f32x4 (&o)[NT][kN]) {
+  const int lane = threadIdx.x % kWave, col = lane % 16, g = lane / 16;
+#pragma unroll 1
+  for (int k = 0; k < 32 && key + k < key1; ++k) {
+    float p[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const uint32_t two = k & 4 ? (k & 2 ? w[t][3] : w[t][2]) : (k & 2 ? w[t][1] : w[t][0]);
+      p[t] = E::value((uint32_t)__shfl((int)two, k / 8 * 16 + col) >> (16 * (k & 1)) & 0xFFFFu);
+    }
+    const uint16_t* at = values + (k / 8 * 16 + g * 4) * 8 + k % 8;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = E::value(at[i * 512 + e * 8]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) o[t][i][e] = key + k < lim[t] ? fmaf(p[t], v, o[t][i][e]) : o[t][i][e];
+      }
+  }
+}
+
+// A stretch of a set's keys, for one key head: where the pages' parts of it stand.
+struct Stretch {
+  const int32_t* list;
+  int64_t base;  // of the layer and head
+  int lo, hi;
+  __device__ int page(const CacheView& c, int key) const {
+    return key < hi ? min((uint32_t)list[key >> c.shift], (uint32_t)(c.n_pages - 1)) : 0;
+  }
+  // bytes from a plane's start to the 32 keys from `key` on, which lie in `page`
+  __device__ int64_t at(const CacheView& c, int page, int key) const {
+    return 2 * (base + page * c.page_elems() + (int64_t)(key & (c.page() - 1)) * c.head_dim);
+  }
+};
+__device__ inline Stretch stretch(const AttendArgs& a, const AttendSet& set, int head, int blk, int cnt) {
+  return Stretch{a.c.table + (int64_t)set.slot * a.c.max_pages, a.base + head * a.c.head_elems(),
+                 set.key0 + blk * kBlock, min(set.key0 + (blk + cnt) * kBlock, set.key1)};
+}
+
+// A narrow set: the waves take the tiles of 32 keys in turn, each for all of its up to
+// NT * 16 rows, with the next tile's keys and values on the way into registers, and
+// join at the end.
+template <int D, int NT>
+struct Meet {
+  f32x4 o[kWaves][D / 16][kWave];
+  float m[kWaves][NT * 16], l[kWaves][NT * 16];
+};
+template <typename E, int D, int NT, int kMax>
+__device__ inline void narrow_set(const AttendArgs& a, const AttendSet& set, const Cursor& at, int cnt,
+                                  Meet<D, kMax>& red) {
+  constexpr int kC = D / 32, kN = D / 16;
+  const CacheView& c = a.c;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int col = lane % 16, g = lane / 16;
+  const Stretch keys = stretch(a, set, at.head, at.blk, cnt);
+  u32x4 kf[2][kC], vf[kN];
+  const auto bring_keys = [&](int page, int key) {
+    const u32x4* p = (const u32x4*)(c.k + keys.at(c, page, key)) + lane;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < kC; ++i) kf[h][i] = p[(h * kC + i) * kWave];
+  };
+  const auto bring_values = [&](int page, int key) {
+    const u32x4* p = (const u32x4*)(c.v + keys.at(c, page, key)) + lane;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) vf[i] = p[i * kWave];
+  };
+  constexpr int kStep = kWaves * 32;
+  int key = keys.lo + wave * 32;
+  int page = keys.page(c, key), next = keys.page(c, key + kStep);
+  if (key < keys.hi) {
+    bring_keys(page, key);
+    bring_values(page, key);
+  }
+  u32x4 q[NT][kC];
+  int lim[NT];
+  f32x4 o[NT][kN];
+  float m[NT], l[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const Row row = row_at(a, set, at.head, t * 16 + col);
+    lim[t] = row.lim;
+#pragma unroll
+    for (int i = 0; i < kC; ++i)
+      q[t][i] = row.q >= 0 ? *(const u32x4*)(a.q + 2 * (row.q + i * 32 + g * 8)) : u32x4{0, 0, 0, 0};
+    m[t] = kLowest, l[t] = 0;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) o[t][i] = f32x4{0, 0, 0, 0};
+  }
+  for (; key < keys.hi; key += kStep) {
+    const bool edge = key + 32 > set.base + 1;  // some row does not see all keys
+    const bool more = key + kStep < keys.hi;
+    f32x4 z[NT][2];
+    u32x4 w[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) score<E>(kf[h], q[t], z[t][h]);
+    if (more) bring_keys(next, key + kStep);
+    if (!edge) {
+      weigh<E, false>(z, w, a.scale, key + g * 8, lim, m, l, o);
+      mix<E>([&](int i) { return vf[i]; }, w, o);
+    } else {
+      weigh<E, true>(z, w, a.scale, key + g * 8, lim, m, l, o);
+      if (!mix_edge<E>([&](int i) { return vf[i]; }, w, key, set.key1, o))
+        mix_slowly<E>((const uint16_t*)(c.v + keys.at(c, page, key)), w, key, set.key1, lim, o);
+    }
+    if (more) bring_values(next, key + kStep);
+    page = next;
+    next = keys.page(c, key + 2 * kStep);
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l[t] += lane_xor<16>(l[t]);
+    l[t] += lane_xor<32>(l[t]);
+    if (lane < 16) {
+      red.m[wave][t * 16 + lane] = m[t];
+      red.l[wave][t * 16 + lane] = l[t];
+    }
+  }
+  __syncthreads();
+  const int64_t part = at.part();
+  const bool whole = set.alone && cnt == set.blocks();
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int j = t * 16 + col;
+    float top = kLowest, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) top = fmaxf(top, red.m[w][j]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += red.l[w][j] * __builtin_amdgcn_exp2f(red.m[w][j] - top);
+    const float mine = __builtin_amdgcn_exp2f(m[t] - top);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) red.o[wave][i][lane] = o[t][i] * mine;
+    __syncthreads();
+    if (j < set.n) {
+      const float norm = 1.0f / sum;
+      char* out = a.out + 2 * (whole ? row_at(a, set, at.head, j).out : 0);
+#pragma unroll
+      for (int i0 = 0; i0 < (kN + kWaves - 1) / kWaves; ++i0) {
+        const int i = i0 * kWaves + wave;
+        if (i >= kN) break;
+        f32x4 all = red.o[0][i][lane];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) all += red.o[w][i][lane];
+        if (whole) put4<E>(out + 2 * (i * 16 + g * 4), all, norm);
+        else *(f32x4*)(a.part_o[kNarrow] + (part * kMax * 16 + j) * D + i * 16 + g * 4) = all;
+      }
+      if (!whole && wave == 0 && g == 0)
+        *(f32x2*)(a.part_ml[kNarrow] + (part * kMax * 16 + j) * 2) = f32x2{top, sum};
+    }
+    __syncthreads();
+  }
+}
+
+// A workgroup goes over a piece of the narrow line, set by set.
+template <typename E, int D, int NT>
+__global__ __launch_bounds__(kThreads) void k_attend(AttendArgs a) {
+  __shared__ Meet<D, NT> red;
+  Cursor at;
+  if (!begin(a, kNarrow, at)) return;
+  while (at.x < at.end) {
+    const AttendSet set = a.p.sets[kNarrow][at.s];
+    const int cnt = (int)min((int64_t)(set.blocks() - at.blk), at.end - at.x);
+    if (NT == 1 || set.n <= 16) narrow_set<E, D, 1, NT>(a, set, at, cnt, red);
+    else if (NT == 2 || set.n <= 32) narrow_set<E, D, NT < 2 ? NT : 2, NT>(a, set, at, cnt, red);
+    else if (set.n <= 48) narrow_set<E, D, NT < 3 ? NT : 3, NT>(a, set, at, cnt, red);
+    else narrow_set<E, D, NT, NT>(a, set, at, cnt, red);
+    advance(at, cnt);
+  }
+}
+
+// A workgroup goes over a piece of the wide line: its waves share the set's tiles of
+// 16 rows, NT each, and a tile of keys and values stands in LDS, brought there past the
+// registers while the one before it is in use.  Two workgroups a CU, so that one's
+// products run under the other's exponentials: that bounds NT, by 256 registers.
+__device__ inline void to_lds(const char* from, void* to) {  // 16 bytes a lane, side by side
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
+                                   (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+template <typename E, int D, int NT>
+__global__ __launch_bounds__(kThreads, 2) void k_attend_wide(AttendArgs a) {
+  constexpr int kC = D / 32, kN = D / 16, kF = 2 * kC + kN;  // KiB of 32 keys
+  constexpr int kU = D > 128 ? 1 : 2, kKeys = 32 * kU;       // of a tile
+  __shared__ u32x4 tile[2][kU][kF][kWave];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
+  const int col = lane % 16, g = lane / 16;
+  const CacheView& c = a.c;
+  Cursor at;
+  if (!begin(a, kWide, at)) return;
+  while (at.x < at.end) {
+    const AttendSet set = a.p.sets[kWide][at.s];
+    const int nb = set.blocks();
+    const int cnt = (int)min((int64_t)(nb - at.blk), at.end - at.x);
+    const Stretch keys = stretch(a, set, at.head, at.blk, cnt);
+    int page[kU];  // of the tile to bring next
+    const auto look = [&](int key) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) page[u] = keys.page(c, key + 32 * u);
+    };
+    const auto bring = [&](int key, int stage) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (key + 32 * u >= keys.hi) break;
+        const int64_t from = keys.at(c, page[u], key + 32 * u) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < kF / kWaves; ++i) {
+          const int f = i * kWaves + wave;
+          to_lds(f < 2 * kC ? c.k + from + f * 1024 : c.v + from + (f - 2 * kC) * 1024, &tile[stage][u][f][0]);
+        }
+      }
+    };
+    static_assert(kF % kWaves == 0, "a tile in equal parts");
+    look(keys.lo);
+    __syncthreads();  // the last set's tiles are done with
+    bring(keys.lo, 0);
+    look(keys.lo + kKeys);
+    u32x4 q[NT][kC];
+    int lim[NT];
     f32x4 o[NT][kN];
     float m[NT], l[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      m[t] = -INFINITY, l[t] = 0;
+      const Row row = row_at(a, set, at.head, (t * kWaves + wave) * 16 + col);
+      lim[t] = row.lim;
+#pragma unroll
+      for (int i = 0; i < kC; ++i)
+        q[t][i] = row.q >= 0 ? *(const u32x4*)(a.q + 2 * (row.q + i * 32 + g * 8)) : u32x4{0, 0, 0, 0};
+      m[t] = kLowest, l[t] = 0;
 #pragma unroll
       for (int i = 0; i < kN; ++i) o[t][i] = f32x4{0, 0, 0, 0};
     }
-    // ---- its keys
-    const int32_t* list = c.table + (int64_t)set.slot * c.max_pages;
-    const int lo = set.key0 + blk * kBlock, hi = min(set.key0 + (blk + cnt) * kBlock, set.key1);
-    for (int key = lo + wave * 32; key < hi; key += kWaves * 32) {
-      const uint32_t page = min((uint32_t)list[key >> c.shift], (uint32_t)(c.n_pages - 1));
-      const int64_t at = a.base + page * c.page_elems() + head * c.head_elems() +
-                         (int64_t)(key & (c.page() - 1)) * D;
-      const u32x4* kp = (const u32x4*)(c.k + 2 * at) + lane;
-      const u32x4* vp = (const u32x4*)(c.v + 2 * at) + lane;
-      u32x4 kf[2][kC], vf[kN];
+    int stage = 0;
+    for (int key = keys.lo; key < keys.hi; key += kKeys, stage ^= 1) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();  // every wave's part of the tile is there, and the tile before done with
+      if (key + kKeys < keys.hi) bring(key + kKeys, stage ^ 1);
+      look(key + 2 * kKeys);
+      const bool edge = key + kKeys > set.base + 1;  // some row does not see all keys
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < kC; ++i) kf[h][i] = kp[(h * kC + i) * kWave];
-#pragma unroll
-      for (int i = 0; i < kN; ++i) vf[i] = vp[i * kWave];
-      const bool edge = key + 32 > set.base + 1;  // some row does not see all keys
-      bool odd = false;                           // values that are not finite
-      if (edge) {
-        // nothing behind the last key has been written for this session
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (key + g * 8 + e >= set.key1) vf[i][e / 2] &= e % 2 ? 0x0000FFFFu : 0xFFFF0000u;
-            odd |= (vf[i][e / 2] >> (16 * (e % 2)) & E::kExp) == E::kExp;
-          }
-        odd = __any(odd);
-      }
-      u32x4 w[NT];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        f32x4 z[2];
+      for (int u = 0; u < kU; ++u) {
+        f32x4 z[NT][2];
+        u32x4 w[NT];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          z[h] = f32x4{0, 0, 0, 0};
+          u32x4 kf[kC];
 #pragma unroll
-          for (int i = 0; i < kC; ++i) z[h] = E::mfma(kf[h][i], q[t][i], z[h]);
+          for (int i = 0; i < kC; ++i) kf[i] = tile[stage][u][h * kC + i][lane];
+#pragma unroll
+          for (int t = 0; t < NT; ++t) score<E>(kf, q[t], z[t][h]);
         }
-        if (edge) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (key + g * 8 + e >= lim[t]) z[e / 4][e % 4] = -INFINITY;
-        }
-        float top = z[0][0];
-#pragma unroll
-        for (int e = 1; e < 8; ++e) top = fmaxf(top, z[e / 4][e % 4]);
-        top = fmaxf(top, lane_xor<16>(top));
-        top = fmaxf(top, lane_xor<32>(top));
-        const float now = fmaxf(m[t], top * a.scale);
-        const float use = now == -INFINITY ? 0.0f : now;  // a row that has seen nothing
-        const float keep = __builtin_amdgcn_exp2f(m[t] - use);
-        m[t] = now;
-        float p[8], sum = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(fmaf(z[e / 4][e % 4], a.scale, -use));
-          sum += p[e];
-        }
-        l[t] = l[t] * keep + sum;
-#pragma unroll
-        for (int i = 0; i < kN; ++i) o[t][i] *= keep;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[t][e] = pack2<E>(p[2 * e], p[2 * e + 1]);
-      }
-      if (!odd) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i)
-#pragma unroll
-          for (int t = 0; t < NT; ++t) o[t][i] = E::mfma(vf[i], w[t], o[t][i]);
-      } else {
-        // key by key, so that a value that is not finite reaches only rows that see it
-        for (int u = 0; u < 32; ++u) {
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            u32x4 one;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              one[e] = vf[i][e] & ((g * 8 + 2 * e == u ? 0x0000FFFFu : 0u) |
-                                   (g * 8 + 2 * e + 1 == u ? 0xFFFF0000u : 0u));
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-              const f32x4 with = E::mfma(one, w[t], o[t][i]);
-              if (key + u < lim[t]) o[t][i] = with;
-            }
-          }
+        const int key32 = key + 32 * u;
+        const auto values = [&](int i) { return tile[stage][u][2 * kC + i][lane]; };
+        if (!edge) {
+          weigh<E, false>(z, w, a.scale, 0, lim, m, l, o);
+          mix<E>(values, w, o);
+        } else if (key32 < keys.hi) {
+          weigh<E, true>(z, w, a.scale, key32 + g * 8, lim, m, l, o);
+          if (!mix_edge<E>(values, w, key32, set.key1, o))
+            mix_slowly<E>((const uint16_t*)&tile[stage][u][2 * kC], w, key32, set.key1, lim, o);
         }
       }
     }
-    // ---- the waves' results joined
+    const int64_t part = at.part();
+    const bool whole = set.alone && cnt == nb;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       l[t] += lane_xor<16>(l[t]);
       l[t] += lane_xor<32>(l[t]);
-      if (lane < 16) {
-        red_m[wave][t * 16 + lane] = m[t];
-        red_l[wave][t * 16 + lane] = l[t];
+      const int j = (t * kWaves + wave) * 16 + col;
+      if (j >= set.n) continue;
+      const float norm = 1.0f / l[t];
+      char* out = a.out + 2 * (whole ? row_at(a, set, at.head, j).out : 0);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        if (whole) put4<E>(out + 2 * (i * 16 + g * 4), o[t][i], norm);
+        else *(f32x4*)(a.part_o[kWide] + (part * a.rows[kWide] + j) * D + i * 16 + g * 4) = o[t][i];
       }
+      if (!whole && g == 0) *(f32x2*)(a.part_ml[kWide] + (part * a.rows[kWide] + j) * 2) = f32x2{m[t], l[t]};
     }
-    __syncthreads();
-    const int64_t part = (int64_t)s * c.n_kv + head + blockIdx.x;
-    const bool whole = set.alone && cnt == nb;
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int j = t * 16 + col;
-      float top = -INFINITY, sum = 0;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, red_m[w][j]);
-      const float use = top == -INFINITY ? 0.0f : top;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) sum += red_l[w][j] * __builtin_amdgcn_exp2f(red_m[w][j] - use);
-      const float mine = __builtin_amdgcn_exp2f(m[t] - use);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) red[wave][i][lane] = o[t][i] * mine;
-      __syncthreads();
-      if (j < set.n) {
-        const float norm = 1.0f / sum;
-#pragma unroll
-        for (int i0 = 0; i0 < (kN + kWaves - 1) / kWaves; ++i0) {
-          const int i = i0 * kWaves + wave;
-          if (i >= kN) break;
-          f32x4 all = red[0][i][lane];
-#pragma unroll
-          for (int w = 1; w < kWaves; ++w) all += red[w][i][lane];
-          if (whole) {
-            uint2 y;
-            y.x = pack2<E>(all[0] * norm, all[1] * norm);
-            y.y = pack2<E>(all[2] * norm, all[3] * norm);
-            *(uint2*)(a.out + 2 * (out_at[t] + i * 16 + g * 4)) = y;
-          } else {
-            *(f32x4*)(a.part_o + (part * a.per + j) * D + i * 16 + g * 4) = all;
-          }
-        }
-        if (!whole && wave == 0 && g == 0)
-          *(f32x2*)(a.part_ml + (part * a.per + j) * 2) = f32x2{top, sum};
-      }
-      __syncthreads();
-    }
-    x += cnt;
-    blk = 0;
-    if (++head == c.n_kv) head = 0, ++s;
+    advance(at, cnt);
   }
 }
 
+// x / piece, in 32 bits where the whole line fits them: the quotient is on the way
+// of every row.
+__device__ inline int piece_of(int64_t x, int64_t total, int64_t piece) {
+  return total >> 32 ? (int)(x / piece) : (int)((uint32_t)x / (uint32_t)piece);
+}
+
 // Joins the partial results of every row; a wave a row and head.  NaN where the
-// session failed.
+// session failed.  The parts' weights come first, a lane a part, so that the loads of
+// their values do not wait for one another.
 template <typename E, int D>
 __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a) {
   constexpr int kVec = D % 128 == 0 ? D / 64 : D == 96 ? 2 : 1;  // elements a lane
   const int lane = threadIdx.x % kWave;
   const CacheView& c = a.c;
   const int b = blockIdx.x / a.R, r = blockIdx.x % a.R;
+  const int heads = a.G * c.n_kv, hq = blockIdx.y * kWaves + threadIdx.x / kWave;
   const AttendSession ss = a.p.sess[b];
-  const int heads = a.G * c.n_kv;
-  if (ss.status == 0 && r >= ss.n) return;
-  const int64_t total = a.p.head->total, piece = a.p.head->piece;
-  (void)total;
-  for (int hq = threadIdx.x / kWave + blockIdx.y * kWaves; hq < heads; hq += kWaves * gridDim.y) {
-    char* out = a.out + 2 * (((int64_t)blockIdx.x * heads + hq) * D + lane * kVec);
-    float o[kVec], m = -INFINITY, l = 0;
+  const AttendHead lines = *a.p.head;
+  if (hq >= heads || (ss.status == 0 && r >= ss.n)) return;
+  const bool mine = lane * kVec < D;
+  float o[kVec], m = kLowest, l = ss.status == 0 ? 0 : NAN;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) o[i] = 0;
-    bool done = false;
-    if (ss.status == 0) {
+  for (int i = 0; i < kVec; ++i) o[i] = 0;
+  if (ss.status == 0) {
+    const int head = hq / a.G;
 #pragma unroll
-      for (int level = 0; level < 3; ++level) {
-        const int first = level < 2 ? ss.node[level] : ss.leaf;
-        if (first < 0) continue;
-        const int j = (ss.t0 + r - a.p.sets[first].t0) * a.G + hq % a.G;
-        const int s = first + j / a.per, row = j % a.per, head = hq / a.G;
-        const AttendSet& set = a.p.sets[s];
-        const int nb = set.blocks();
-        const int64_t x = set.cum * c.n_kv + (int64_t)head * nb;
-        const int p0 = (int)(x / piece), p1 = (int)((x + nb - 1) / piece);
-        if (set.alone && p0 == p1) done = true;
-        if (done) break;
-        for (int p = p0; p <= p1; ++p) {
-          const int64_t at = ((int64_t)s * c.n_kv + head + p) * a.per + row;
-          const f32x2 ml = *(const f32x2*)(a.part_ml + at * 2);
-          const float now = fmaxf(m, ml[0]), use = now == -INFINITY ? 0.0f : now;
-          const float old = __builtin_amdgcn_exp2f(m - use), add = __builtin_amdgcn_exp2f(ml[0] - use);
-          m = now;
-          l = l * old + ml[1] * add;
-          if (lane * kVec < D) {
-            const float* y = a.part_o + at * D + lane * kVec;
+    for (int level = 0; level < 3; ++level) {
+      if (ss.first[level] < 0) continue;
+      const int first = ss.first[level] / 2, line = ss.first[level] % 2;
+      const AttendSet* sets = a.p.sets[line];
+      // a session's own sets begin with its first row, a run's with the run's
+      const int t0 = level < 2 ? sets[first].t0 : ss.t0;
+      const int per = sets[first].per;
+      const int j = (ss.t0 + r - t0) * a.G + hq % a.G;
+      const int s = first + j / per, row = j % per;
+      const int nb = sets[first].blocks();
+      const int64_t blocks = line ? lines.blocks[1] : lines.blocks[0];
+      const int64_t x = head * blocks + sets[first].cum + (int64_t)(j / per) * nb;
+      const int64_t total = line ? lines.total[1] : lines.total[0];
+      const int64_t piece = line ? lines.piece[1] : lines.piece[0];
+      const int p0 = piece_of(x, total, piece), parts = piece_of(x + nb - 1, total, piece) - p0 + 1;
+      if (parts == 1 && sets[first].alone) return;
+      const int rows = line ? a.rows[1] : a.rows[0];
+      const float* part_ml = line ? a.part_ml[1] : a.part_ml[0];
+      const float* part_o = line ? a.part_o[1] : a.part_o[0];
+      const int n_sets = line ? lines.sets[1] : lines.sets[0];
+      const int64_t at = ((int64_t)head * n_sets + s + p0) * rows + row;
+      for (int i0 = 0; i0 < parts; i0 += kWave) {
+        const int n = min(parts - i0, kWave);
+        f32x2 ml = {kLowest, 0};
+        if (lane < n) ml = *(const f32x2*)(part_ml + (at + (int64_t)(i0 + lane) * rows) * 2);
+        const float now = fmaxf(m, wave_reduce(ml[0], OpMax()));
+        const float old = __builtin_amdgcn_exp2f(m - now), w = __builtin_amdgcn_exp2f(ml[0] - now);
+        m = now;
+        l = l * old + wave_reduce(ml[1] * w, OpAdd());
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) o[i] = o[i] * old + y[i] * add;
+        for (int i = 0; i < kVec; ++i) o[i] *= old;
+        const float* y = part_o + (at + (int64_t)i0 * rows) * D + (mine ? lane * kVec : 0);
+        constexpr int kStep = 8;
+        for (int k0 = 0; k0 < n; k0 += kStep) {
+          float v[kStep][kVec];
+#pragma unroll
+          for (int k = 0; k < kStep; ++k)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) v[k][i] = y[(int64_t)min(k0 + k, n - 1) * rows * D + i];
+#pragma unroll
+          for (int k = 0; k < kStep; ++k) {
+            const float wk = lane_read(w, min(k0 + k, n - 1));
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) o[i] = k0 + k < n ? fmaf(v[k][i], wk, o[i]) : o[i];
           }
         }
       }
-    } else {
-      l = NAN;
     }
-    if (done || lane * kVec >= D) continue;
-    const float norm = 1.0f / l;
-    if constexpr (kVec == 1) {
-      *(uint16_t*)out = (uint16_t)pack2<E>(o[0] * norm, 0);
-    } else {
+  }
+  if (!mine) return;
+  char* out = a.out + 2 * (((int64_t)blockIdx.x * heads + hq) * D + lane * kVec);
+  const float norm = 1.0f / l;
+  if constexpr (kVec == 1) {
+    *(uint16_t*)out = (uint16_t)pack2<E>(o[0] * norm, 0);
+  } else {
 #pragma unroll
-      for (int i = 0; i < kVec; i += 2) *(uint32_t*)(out + 2 * i) = pack2<E>(o[i] * norm, o[i + 1] * norm);
-    }
+    for (int i = 0; i < kVec; i += 2) *(uint32_t*)(out + 2 * i) = pack2<E>(o[i] * norm, o[i + 1] * norm);
   }
 }
 
 template <typename E, int D>
 void launch(const AttendArgs& a, hipStream_t st) {
-  if (a.per == 16)
+  // rows that neighbours share go together, which may make them many
+  if (a.B > 1 || a.R * a.G > a.rows[kNarrow])
+    hipLaunchKernelGGL((k_attend_wide<E, D, wide_tiles(D)>), dim3(kPieces), dim3(kThreads), 0, st, a);
+  if (a.rows[kNarrow] == 16)
     hipLaunchKernelGGL((k_attend<E, D, 1>), dim3(kPieces), dim3(kThreads), 0, st, a);
-  else if (a.per == 32)
+  else if (a.rows[kNarrow] == 32)
     hipLaunchKernelGGL((k_attend<E, D, 2>), dim3(kPieces), dim3(kThreads), 0, st, a);
   else if constexpr (D <= 128)
     hipLaunchKernelGGL((k_attend<E, D, 4>), dim3(kPieces), dim3(kThreads), 0, st, a);
-  const int heads = a.G * a.c.n_kv;
-  const unsigned gy = (heads + 8 * kWaves - 1) / (8 * kWaves);
+  const unsigned gy = (a.G * a.c.n_kv + kWaves - 1) / kWaves;
   hipLaunchKernelGGL((k_join<E, D>), dim3(a.B * a.R, gy), dim3(kThreads), 0, st, a);
 }
 template <typename E>
@@ -331,7 +596,21 @@ void launch_dim(const AttendArgs& a, hipStream_t st) {
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= ((int64_t)1 << 40); }
 
 // Slots for partial results: one a set and head, and one for every cut.
-int64_t slots_of(const sv_cache* c, int64_t sets) { return sets * c->n_kv + kPieces; }
+struct Parts {
+  int64_t slots[2], bytes;
+  int32_t rows[2];
+};
+Parts parts_of(const sv_cache* c, const PlanSizes& z, int32_t R, int32_t G) {
+  Parts p;
+  p.rows[kNarrow] = narrow_rows((int64_t)R * G, c->head_dim);
+  p.rows[kWide] = wide_rows(c->head_dim);
+  p.bytes = 0;
+  for (int line = 0; line < 2; ++line) {
+    p.slots[line] = z.sets[line] * c->n_kv + kPieces;
+    p.bytes += p.slots[line] * p.rows[line] * (c->head_dim + 2) * 4;
+  }
+  return p;
+}
 
 }  // namespace
 }  // namespace sv
@@ -340,9 +619,8 @@ extern "C" size_t sv_cache_attention_bytes(const sv_cache* cache, int32_t n_head
                                            int32_t R) {
   using namespace sv;
   if (sv_cache_plan_bytes(cache, n_heads, B, R) == 0) return 0;
-  const int G = n_heads / cache->n_kv, per = rows_of_set((int64_t)R * G, cache->head_dim);
-  const int64_t slots = slots_of(cache, plan_sizes(B, R, G, per).sets);
-  return (size_t)(slots * per * (cache->head_dim + 2) * 4);
+  const int G = n_heads / cache->n_kv;
+  return (size_t)parts_of(cache, plan_sizes(B, R, G, cache->head_dim), R, G).bytes;
 }
 
 extern "C" int sv_cache_attention(const sv_cache* cache, int32_t layer, const void* q,
@@ -358,12 +636,19 @@ extern "C" int sv_cache_attention(const sv_cache* cache, int32_t layer, const vo
   if (!stride_ok(q_session) || !stride_ok(q_row) || !stride_ok(q_head)) return SV_ERR_ARG;
   if (!(scale > 0) || !(scale < INFINITY)) return SV_ERR_ARG;
   if (workspace_bytes < need) return SV_ERR_WORKSPACE;
-  const int G = n_heads / cache->n_kv, per = rows_of_set((int64_t)R * G, cache->head_dim);
-  const PlanSizes z = plan_sizes(B, R, G, per);
+  const int G = n_heads / cache->n_kv;
+  const PlanSizes z = plan_sizes(B, R, G, cache->head_dim);
+  const Parts parts = parts_of(cache, z, R, G);
   AttendArgs a = {view_of(cache), plan_of(z, (void*)plan), (const char*)q, q_session, q_row, q_head,
-                  (char*)out, (float*)workspace, nullptr, scale * 1.44269504088896340736f, 0, G, B,
-                  R, per};
-  a.part_ml = a.part_o + slots_of(cache, z.sets) * per * cache->head_dim;
+                  (char*)out, {}, {}, {parts.rows[0], parts.rows[1]},
+                  scale * 1.44269504088896340736f, 0, G, B, R};
+  float* part = (float*)workspace;
+  for (int line = 0; line < 2; ++line) {
+    const int64_t rows = parts.slots[line] * parts.rows[line];
+    a.part_o[line] = part;
+    a.part_ml[line] = part + rows * cache->head_dim;
+    part += rows * (cache->head_dim + 2);
+  }
   a.base = layer * a.c.layer_elems();
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();

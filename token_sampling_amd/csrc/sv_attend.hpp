@@ -1,24 +1,30 @@
 // sv_attend.hpp -- the plan of a round's attention (sv_cache_plan), as the
 // attention's kernels read it.
 //
-// A set is up to kRows query rows (a row here is a round's row and a query head
-// of the set's key head) that go over the same keys: a block of one session's
-// rows over the keys that it has alone, or of the rows of neighbouring sessions
-// over keys that they share.  Keys are counted in blocks of kBlock.  The sets'
-// blocks, for every key head, stand in one line, which is cut into equal pieces, a
-// piece a workgroup: piece i leaves a partial result (largest score, sum, weighted
-// values) for every set and head that it touches, in slot set * n_kv + head + i, and
-// where a set and head lie in one piece and nothing else belongs to their rows, the
-// result itself.
+// A set is a number of query rows (a row here is a round's row and a query head of
+// the set's key head) that go over the same keys: one session's rows over the keys
+// that it has alone, or rows of neighbouring sessions over keys that they share.
+// Where they fit one wave's registers the set is narrow: the waves of a workgroup
+// take its keys in turn, and what counts is the bytes that arrive.  Else it is
+// wide: the waves take its rows, and share the keys in LDS.  Keys are counted in
+// blocks of kBlock.  The narrow sets' blocks stand in one line, the first key head's,
+// then the second's and so on, the wide sets' in another; a line is cut into equal
+// pieces, a piece a workgroup.  Piece i leaves a partial result (largest score, sum,
+// weighted values) for every set and head that it touches, in slot head * sets + set
+// + i, and where a set and head lie in one piece and nothing else belongs to their
+// rows, the result itself.
+// An XCD has neighbouring pieces (its workgroups are every eighth): sets of many rows
+// over the same keys go over a head's keys in one L2.
 #pragma once
 
 #include "sv_cache.hpp"
 
 namespace sv {
 
-constexpr int kBlock = 128;       // keys
-constexpr int kPieces = 512;      // workgroups: two a CU
-constexpr int kFar = 1 << 30;     // no limit on keys
+constexpr int kBlock = 128;     // keys
+constexpr int kNarrow = 0, kWide = 1;
+constexpr int kPieces = 512;    // of a line at most: two a CU
+constexpr int kFar = 1 << 30;   // no limit on keys
 
 struct AttendSet {
   int32_t t0;    // the first of the rows' places in row_of
@@ -29,47 +35,55 @@ struct AttendSet {
   int32_t base;  // round row r sees the keys before base + r + 1; kFar: all
   int32_t alone; // nothing else belongs to these rows
   int64_t cum;   // blocks of the sets before
-  int64_t pad;
+  int32_t per;   // rows of each but the last set over the same keys
+  int32_t pad;
   __host__ __device__ int blocks() const { return (key1 - key0 + kBlock - 1) / kBlock; }
 };
 static_assert(sizeof(AttendSet) == 48, "AttendSet layout");
 
+// A session's rows stand in the sets from first[0] (its run's shared keys), first[1]
+// (its run's in that run) and first[2] (its own keys) on: 2 * set + line, -1: none.
 struct AttendSession {
-  int32_t status, n, t0;    // rows in use, their first place in row_of
-  int32_t leaf;             // the first set over the keys of its own; -1: no rows
-  int32_t node[2];          // the first sets over shared keys, -1: none
+  int32_t status, n, t0;  // rows in use, their first place in row_of
+  int32_t first[3];
   int32_t pad[2];
 };
 
 struct AttendHead {
-  int64_t total, piece;  // blocks of all sets and heads, of a piece
-  int32_t n_sets, pad[3];
+  int64_t blocks[2], total[2], piece[2];  // of all sets, of all sets and heads, of a piece
+  int32_t sets[2];
 };
 
 struct AttendPlan {
   AttendHead* head;
-  AttendSession* sess;  // [B]
-  int4* starts;         // [kPieces]: set, key head, block; of pieces that begin before total
-  int32_t* shared;      // [B]: keys shared with the session before
-  int32_t* row_of;      // [B * R]: session * R + round row
-  AttendSet* sets;
+  AttendSession* sess;   // [B]
+  int4* starts[2];       // [kPieces]: set, key head, block; of pieces that begin before total
+  int32_t* shared;       // [B]: keys shared with the session before
+  int32_t* row_of;       // [B * R]: session * R + round row
+  AttendSet* sets[2];
 };
 
-// Query rows of a set.
-inline int rows_of_set(int64_t rows, int head_dim) {
+// Rows of a narrow set at most, by what a round brings; and of a wide one.
+inline int narrow_rows(int64_t rows, int head_dim) {
   if (rows <= 16) return 16;
   if (rows <= 32 || head_dim > 128) return 32;
   return 64;
 }
+constexpr int wide_tiles(int head_dim) {  // tiles of 16 rows, of each of its four waves
+  return head_dim > 128 ? 1 : head_dim > 64 ? 2 : 3;
+}
+inline int wide_rows(int head_dim) { return 64 * wide_tiles(head_dim); }
 
 struct PlanSizes {
-  int64_t sets, bytes, sess, starts, shared, row_of, set_at;
+  int64_t sets[2], bytes, sess, starts, shared, row_of, set_at[2];
 };
-inline PlanSizes plan_sizes(int32_t B, int32_t R, int32_t G, int32_t per) {
+inline PlanSizes plan_sizes(int32_t B, int32_t R, int32_t G, int32_t head_dim) {
   PlanSizes z;
-  // a session's own, and on two levels those of its run of sessions
-  z.sets = (int64_t)B * (((int64_t)R * G + per - 1) / per) +
-           2 * (((int64_t)B * R * G + per - 1) / per + B / 2 + 1);
+  const int64_t rows = (int64_t)R * G, wide = wide_rows(head_dim);
+  const int64_t runs = 2 * ((int64_t)B / 2 + 1);  // of two sessions or more, on two levels
+  z.sets[kNarrow] = B + runs;
+  z.sets[kWide] = 2 * ((B * rows + wide - 1) / wide) + runs;
+  if (rows > narrow_rows(rows, head_dim)) z.sets[kWide] += B * ((rows + wide - 1) / wide);
   int64_t at = 256;
   const auto take = [&at](int64_t n) {
     const int64_t here = at;
@@ -77,17 +91,19 @@ inline PlanSizes plan_sizes(int32_t B, int32_t R, int32_t G, int32_t per) {
     return here;
   };
   z.sess = take((int64_t)B * sizeof(AttendSession));
-  z.starts = take(kPieces * sizeof(int4));
+  z.starts = take(2 * kPieces * sizeof(int4));
   z.shared = take((int64_t)B * 4);
   z.row_of = take((int64_t)B * R * 4);
-  z.set_at = take(z.sets * sizeof(AttendSet));
+  for (int line = 0; line < 2; ++line) z.set_at[line] = take(z.sets[line] * sizeof(AttendSet));
   z.bytes = at;
   return z;
 }
 inline AttendPlan plan_of(const PlanSizes& z, void* p) {
   char* c = (char*)p;
-  return AttendPlan{(AttendHead*)c, (AttendSession*)(c + z.sess), (int4*)(c + z.starts),
-                    (int32_t*)(c + z.shared), (int32_t*)(c + z.row_of), (AttendSet*)(c + z.set_at)};
+  int4* starts = (int4*)(c + z.starts);
+  return AttendPlan{(AttendHead*)c, (AttendSession*)(c + z.sess), {starts, starts + kPieces},
+                    (int32_t*)(c + z.shared), (int32_t*)(c + z.row_of),
+                    {(AttendSet*)(c + z.set_at[0]), (AttendSet*)(c + z.set_at[1])}};
 }
 
 }  // namespace sv

@@ -14,7 +14,9 @@ struct PlanArgs {
   AttendPlan p;
   const int32_t *slots, *rows;
   int32_t* status;
-  int32_t G, B, R, per;  // query heads a key head; rows of a set
+  int32_t G, B, R;       // query heads a key head
+  int32_t narrow, wide;  // rows of a set
+  int32_t pieces[2];
   int32_t least;         // keys shared that are worth a set of their own
 };
 
@@ -56,9 +58,21 @@ __global__ __launch_bounds__(kShared) void k_shared(PlanArgs a) {
   if (threadIdx.x == 0) a.p.shared[b] = keys;
 }
 
+// Rows over the same keys as sets of a line: the number of sets, equal but for the
+// last, in whole tiles of 16 rows.
+struct Cut {
+  int line, n, per;
+};
+__device__ inline Cut cut_rows(const PlanArgs& a, int64_t rows) {
+  if (rows <= a.narrow) return Cut{kNarrow, rows > 0, a.narrow};
+  const int n = (int)((rows + a.wide - 1) / a.wide);
+  return Cut{kWide, n, (int)((rows + n - 1) / n + 15) / 16 * 16};
+}
+
 __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
-  // by session
-  __shared__ int32_t t_at[SV_CACHE_B_MAX + 1], set_at[SV_CACHE_B_MAX];
+  // by session: the first row's place; in each line the first set, and the blocks
+  // before it
+  __shared__ int32_t t_at[SV_CACHE_B_MAX + 1], set_at[2][SV_CACHE_B_MAX + 1];
   __shared__ int64_t cum_at[SV_CACHE_B_MAX];
   // by run, of both levels: first session, shared keys
   __shared__ int32_t first[2][SV_CACHE_B_MAX + 1], depth[2][SV_CACHE_B_MAX];
@@ -84,13 +98,22 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
         if (rows < 0 || rows > a.R) {
           st[i] = SV_S_LIMIT;
         } else if (rows > 0) {
-          // the rows' positions must lie in pages of the session's own
+          // the rows' positions must lie in pages of the session's own: at most
+          // four, looked up side by side
+          static_assert((SV_M_MAX + 1 + 30) / 32 + 1 <= 4, "pages of a round's rows");
           const int64_t at = c.lens[h], end = at + rows;
           const int held = min(c.held[h], c.max_pages);
           bool ok = at >= 0 && end <= (int64_t)held << c.shift;
-          for (int64_t p = at >> c.shift; ok && p <= (end - 1) >> c.shift; ++p) {
-            const int page = c.table[(int64_t)h * c.max_pages + p];
-            ok = page >= 0 && page < c.n_pages && c.refs[page] == 1;
+          if (ok) {
+            const int32_t* list = c.table + (int64_t)h * c.max_pages;
+            const int p0 = (int)(at >> c.shift), p1 = (int)((end - 1) >> c.shift);
+            int page[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) page[k] = list[min(p0 + k, p1)];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              ok = ok & (page[k] >= 0) & (page[k] < c.n_pages) &
+                   (c.refs[min(max(page[k], 0), c.n_pages - 1)] == 1);
           }
           if (ok) {
             n[i] = rows, len[i] = (int)at, slot[i] = h;
@@ -109,7 +132,6 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
   if (tid == 0) t_at[a.B] = (int)rows_all;
 
   // runs of sessions that share their first keys; in them, runs that share more
-  int runs[2];
 #pragma unroll
   for (int level = 0; level < 2; ++level) {
     int64_t before = 0;
@@ -130,101 +152,135 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
       else if (b < a.B) atomicMin(&depth[level][run[level][i]], shared[i]);
       before += total;
     }
-    runs[level] = (int)before;
-    if (tid == 0) first[level][runs[level]] = a.B;
+    if (tid == 0) first[level][before] = a.B;
     __syncthreads();
   }
 
-  // the sets of every session: its runs' where they begin with it, then its own
-  int own[kPer], key0[kPer], k1[kPer], d1[kPer], d2[kPer], n1[kPer], n2[kPer];
-  int64_t sets_all = 0, cum_all = 0;
+  // every session's sets: its runs' where they begin with it, then its own
+  Cut cut[3][kPer];
+  int key[3][kPer];            // where the keys of the three end
+  int64_t cum[2][kPer], sets_all[2] = {0, 0}, cum_all[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (i * kOne >= a.B) break;
     const int b = i * kOne + tid;
-    own[i] = key0[i] = d1[i] = d2[i] = n1[i] = n2[i] = k1[i] = 0;
+    int64_t sets[2] = {0, 0}, blocks[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) cut[k][i] = Cut{0, 0, 16}, key[k][i] = 0;
     if (b < a.B) {
-      const int r1 = run[0][i], r2 = run[1][i];
-      d1[i] = depth[0][r1] == kNone ? 0 : depth[0][r1];
-      d2[i] = depth[1][r2] == kNone ? d1[i] : depth[1][r2];
-      const int64_t rows1 = (int64_t)(t_at[first[0][r1 + 1]] - t_at[first[0][r1]]) * a.G;
-      const int64_t rows2 = (int64_t)(t_at[first[1][r2 + 1]] - t_at[first[1][r2]]) * a.G;
-      if (d1[i] > 0) n1[i] = (int)((rows1 + a.per - 1) / a.per);
-      if (d2[i] > d1[i]) n2[i] = (int)((rows2 + a.per - 1) / a.per);
-      key0[i] = d2[i], k1[i] = len[i] + n[i];
-      if (n[i] > 0) own[i] = (int)(((int64_t)n[i] * a.G + a.per - 1) / a.per);
+      int from = 0;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        bool begins = true;
+        if (k < 2) {
+          const int r = run[k][i], d = depth[k][r] == kNone ? from : depth[k][r];
+          key[k][i] = d;
+          if (d > from) cut[k][i] = cut_rows(a, (int64_t)(t_at[first[k][r + 1]] - t_at[first[k][r]]) * a.G);
+          begins = first[k][r] == b;
+        } else {
+          key[k][i] = len[i] + n[i];
+          cut[k][i] = cut_rows(a, (int64_t)n[i] * a.G);
+        }
+        if (begins && cut[k][i].n > 0) {
+          const int64_t nb = (key[k][i] - from + kBlock - 1) / kBlock;
+          sets[cut[k][i].line] += cut[k][i].n;
+          blocks[cut[k][i].line] += cut[k][i].n * nb;
+        }
+        from = key[k][i];
+      }
     }
-    const int at1 = b < a.B && first[0][run[0][i]] == b ? n1[i] : 0;
-    const int at2 = b < a.B && first[1][run[1][i]] == b ? n2[i] : 0;
-    const int64_t sets = (int64_t)at1 + at2 + own[i];
-    const int64_t blocks = (int64_t)at1 * (d1[i] / kBlock) + (int64_t)at2 * ((d2[i] - d1[i]) / kBlock) +
-                           (int64_t)own[i] * ((k1[i] - key0[i] + kBlock - 1) / kBlock);
-    int64_t total;
-    const int64_t s = sets_all + block_incl_scan<kOne, int64_t>(sets, smem, total) - sets;
-    sets_all += total;
-    const int64_t cum = cum_all + block_incl_scan<kOne, int64_t>(blocks, smem, total) - blocks;
-    cum_all += total;
-    if (b < a.B) {
-      set_at[b] = (int)s;
-      cum_at[b] = cum;
+#pragma unroll
+    for (int line = 0; line < 2; ++line) {
+      int64_t total;
+      const int64_t s = sets_all[line] + block_incl_scan<kOne, int64_t>(sets[line], smem, total) - sets[line];
+      sets_all[line] += total;
+      cum[line][i] = cum_all[line] + block_incl_scan<kOne, int64_t>(blocks[line], smem, total) - blocks[line];
+      cum_all[line] += total;
+      if (b < a.B) set_at[line][b] = (int)s;
     }
   }
+  if (tid < 2) set_at[tid][a.B] = (int)sets_all[tid];
   __syncthreads();
-  // written by a wave a session
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (i * kOne >= a.B) break;
     const int b = i * kOne + tid;
-    if (b < a.B) {
-      const int f1 = first[0][run[0][i]], f2 = first[1][run[1][i]];
-      const bool begins1 = f1 == b, begins2 = f2 == b;
-      int s = set_at[b];
-      int64_t cum = cum_at[b];
-      if (begins1 && n1[i] > 0) {
-        const int rows = (t_at[first[0][run[0][i] + 1]] - t_at[b]) * a.G;
-        // a run's pages are in the list of any of its sessions that has rows
-        for (int k = 0; k < n1[i]; ++k, ++s, cum += d1[i] / kBlock)
-          a.p.sets[s] = AttendSet{t_at[b], k * a.per, min(a.per, rows - k * a.per), 0, d1[i], -1,
-                                  kFar, 0, cum, 0};
+    if (b >= a.B) continue;
+    AttendSession ss = {st[i], n[i], t_at[b], {-1, -1, -1}, {0, 0}};
+    int s[2] = {set_at[0][b], set_at[1][b]};
+    int64_t x[2] = {cum[0][i], cum[1][i]};
+    int from = 0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const Cut& cc = cut[k][i];
+      const int f = k < 2 ? first[k][run[k][i]] : b;
+      if (cc.n > 0) {
+        if (f == b) {
+          const int rows = k < 2 ? (t_at[first[k][run[k][i] + 1]] - t_at[b]) * a.G : n[i] * a.G;
+          // a run's list of pages: that of the session of its first row
+          const int list = k < 2 ? place_of(a, a.p.row_of[t_at[b]] / a.R) : slot[i];
+          const int nb = (key[k][i] - from + kBlock - 1) / kBlock;
+          int at = cc.line ? s[1] : s[0];
+          int64_t y = cc.line ? x[1] : x[0];
+          if (n[i] > 0 || k < 2) ss.first[k] = 2 * at + cc.line;
+          for (int q = 0; q < cc.n; ++q, ++at, y += nb)
+            a.p.sets[cc.line][at] = AttendSet{t_at[b], q * cc.per, min(cc.per, rows - q * cc.per), from,
+                                              key[k][i], list, k < 2 ? kFar : len[i], k == 2 && from == 0,
+                                              y, cc.per, 0};
+          if (cc.line) s[1] = at, x[1] = y;
+          else s[0] = at, x[0] = y;
+        } else {
+          // behind the sets that session f has in this line for a run of the level above
+          int at = set_at[cc.line][f];
+          if (k == 1 && first[0][run[0][i]] == f && cut[0][i].n > 0 && cut[0][i].line == cc.line)
+            at += cut[0][i].n;
+          ss.first[k] = 2 * at + cc.line;
+        }
       }
-      if (begins2 && n2[i] > 0) {
-        const int rows = (t_at[first[1][run[1][i] + 1]] - t_at[b]) * a.G;
-        for (int k = 0; k < n2[i]; ++k, ++s, cum += (d2[i] - d1[i]) / kBlock)
-          a.p.sets[s] = AttendSet{t_at[b], k * a.per, min(a.per, rows - k * a.per), d1[i], d2[i], -1,
-                                  kFar, 0, cum, 0};
-      }
-      const int leaf = s;
-      const int blocks = (k1[i] - key0[i] + kBlock - 1) / kBlock;
-      for (int k = 0; k < own[i]; ++k, ++s, cum += blocks)
-        a.p.sets[s] = AttendSet{t_at[b], k * a.per, min(a.per, n[i] * a.G - k * a.per), key0[i], k1[i],
-                                slot[i], len[i], d2[i] == 0, cum, 0};
-      const int s1 = set_at[f1];
-      const int s2 = set_at[f2] + (first[0][run[0][i]] == f2 ? n1[i] : 0);
-      a.p.sess[b] = AttendSession{st[i], n[i], t_at[b], n[i] > 0 ? leaf : -1,
-                                  {n[i] > 0 && n1[i] > 0 ? s1 : -1, n[i] > 0 && n2[i] > 0 ? s2 : -1},
-                                  {0, 0}};
-      if (a.status) a.status[b] = st[i];
+      from = key[k][i];
     }
+    if (n[i] == 0) ss.first[0] = ss.first[1] = ss.first[2] = -1;
+    a.p.sess[b] = ss;
+    if (a.status) a.status[b] = st[i];
   }
-  __syncthreads();
-  // a run's list of pages: that of the session of its first row
-  for (int64_t s = tid; s < sets_all; s += kOne)
-    if (a.p.sets[s].slot < 0) a.p.sets[s].slot = place_of(a, a.p.row_of[a.p.sets[s].t0] / a.R);
-  const int64_t total = cum_all * c.n_kv;
-  const int64_t piece = (total + kPieces - 1) / kPieces;
-  if (tid == 0) *a.p.head = AttendHead{total, piece, (int32_t)sets_all, {0, 0, 0}};
-  for (int i = tid; i < kPieces; i += kOne) {
-    const int64_t x = i * piece;
-    if (x >= total) continue;
-    int64_t lo = 0, hi = sets_all - 1;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) / 2;
-      if (a.p.sets[mid].cum * c.n_kv <= x) lo = mid;
-      else hi = mid - 1;
+
+  // where each line's pieces begin
+#pragma unroll
+  for (int line = 0; line < 2; ++line) {
+    const int64_t total = cum_all[line] * c.n_kv;
+    const int64_t piece = (total + a.pieces[line] - 1) / a.pieces[line];
+    if (tid == 0) {
+      a.p.head->total[line] = total;
+      a.p.head->piece[line] = piece;
+      a.p.head->blocks[line] = cum_all[line];
+      a.p.head->sets[line] = (int)sets_all[line];
     }
-    const AttendSet& set = a.p.sets[lo];
-    const int64_t in = x - set.cum * c.n_kv;
-    a.p.starts[i] = make_int4((int)lo, (int)(in / set.blocks()), (int)(in % set.blocks()), 0);
+    if (total == 0) continue;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (i * kOne >= a.B) break;
+      if (i * kOne + tid < a.B) cum_at[i * kOne + tid] = cum[line][i];
+    }
+    __syncthreads();
+    const int64_t x = tid * piece;
+    if (tid < a.pieces[line] && x < total) {
+      const int64_t head = x / cum_all[line], y = x - head * cum_all[line];
+      int lo = 0, hi = a.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (cum_at[mid] <= y) lo = mid;
+        else hi = mid - 1;
+      }
+      const AttendSet* sets = a.p.sets[line];
+      hi = set_at[line][lo + 1] - 1, lo = set_at[line][lo];
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (sets[mid].cum <= y) lo = mid;
+        else hi = mid - 1;
+      }
+      a.p.starts[line][tid] = make_int4(lo, (int)head, (int)(y - sets[lo].cum), 0);
+    }
   }
 }
 
@@ -240,7 +296,7 @@ extern "C" size_t sv_cache_plan_bytes(const sv_cache* cache, int32_t n_heads, in
   using namespace sv;
   if (!sizes_ok(cache, n_heads, B, R)) return 0;
   const int G = n_heads / cache->n_kv;
-  return (size_t)plan_sizes(B, R, G, rows_of_set((int64_t)R * G, cache->head_dim)).bytes;
+  return (size_t)plan_sizes(B, R, G, cache->head_dim).bytes;
 }
 
 extern "C" int sv_cache_plan(const sv_cache* cache, const int32_t* slots, const int32_t* rows,
@@ -250,12 +306,13 @@ extern "C" int sv_cache_plan(const sv_cache* cache, const int32_t* slots, const 
   if (!sizes_ok(cache, n_heads, B, R) || !sessions_ok(cache, slots, B) || !plan) return SV_ERR_ARG;
   if ((uintptr_t)plan % 16 != 0) return SV_ERR_ARG;
   const int G = n_heads / cache->n_kv;
-  const int per = rows_of_set((int64_t)R * G, cache->head_dim);
-  const PlanSizes z = plan_sizes(B, R, G, per);
+  const PlanSizes z = plan_sizes(B, R, G, cache->head_dim);
   if (plan_bytes < (size_t)z.bytes) return SV_ERR_WORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
-  const PlanArgs a = {view_of(cache), plan_of(z, plan), slots, rows, status, G, B, R, per, 256};
+  const PlanArgs a = {view_of(cache), plan_of(z, plan), slots, rows, status, G, B, R,
+                      narrow_rows((int64_t)R * G, cache->head_dim), wide_rows(cache->head_dim),
+                      {kPieces, kPieces}, 256};
   hipLaunchKernelGGL(k_shared, dim3(B), dim3(kShared), 0, st, a);
   hipLaunchKernelGGL(k_plan, dim3(1), dim3(kOne), 0, st, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_DEVICE;
