@@ -89,7 +89,7 @@ struct Cursor {
 constexpr int kXcds = 8;
 __device__ inline bool begin(const AttendArgs& a, int line, Cursor& at) {
   const int64_t total = a.p.head->total[line], piece = a.p.head->piece[line];
-  at.piece = blockIdx.x % kXcds * (kPieces / kXcds) + blockIdx.x / kXcds;
+  at.piece = blockIdx.x % kXcds * (kPieces[line] / kXcds) + blockIdx.x / kXcds;
   at.sets = a.p.head->sets[line];
   at.x = at.piece * piece;
   at.end = min(at.x + piece, total);
@@ -119,10 +119,10 @@ __device__ inline void score(const u32x4 (&kf)[kC], const u32x4 (&q)[kC], f32x4&
 // costs no digits in binary32 or in either 16-bit type.
 constexpr float kSlack = 8.0f;
 constexpr float kLowest = -3.402823466e38f;  // m of a row that has seen nothing
-template <typename E, bool kEdge, int NT, int kN>
-__device__ inline void weigh(f32x4 (&z)[NT][2], u32x4 (&w)[NT], float scale, int key, const int (&lim)[NT],
-                             float (&m)[NT], float (&l)[NT], f32x4 (&o)[NT][kN]) {
-  float top[NT];
+// Hidden scores are -inf; true where a row's m has to follow.
+template <bool kEdge, int NT>
+__device__ inline bool look_up(f32x4 (&z)[NT][2], float (&top)[NT], float scale, int key, const int (&lim)[NT],
+                               const float (&m)[NT]) {
   bool far = false;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -137,29 +137,46 @@ __device__ inline void weigh(f32x4 (&z)[NT][2], u32x4 (&w)[NT], float scale, int
     top[t] *= scale;
     far |= top[t] > m[t] + kSlack;
   }
-  if (__any(far)) {
+  return __any(far);
+}
+template <int NT, int kN>
+__device__ inline void follow(const float (&top)[NT], float (&m)[NT], float (&l)[NT], f32x4 (&o)[NT][kN]) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float now = fmaxf(top[t], lane_xor<16>(top[t]));
-      now = fmaxf(m[t], fmaxf(now, lane_xor<32>(now)));
-      const float keep = __builtin_amdgcn_exp2f(m[t] - now);
-      m[t] = now;
-      l[t] *= keep;
+  for (int t = 0; t < NT; ++t) {
+    float now = fmaxf(top[t], lane_xor<16>(top[t]));
+    now = fmaxf(m[t], fmaxf(now, lane_xor<32>(now)));
+    const float keep = __builtin_amdgcn_exp2f(m[t] - now);
+    m[t] = now;
+    l[t] *= keep;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) o[t][i] *= keep;
-    }
+    for (int i = 0; i < kN; ++i) o[t][i] *= keep;
   }
+}
+// The weights, and their sums.
+template <typename E, int NT>
+__device__ inline void powers(const f32x4 (&z)[NT][2], u32x4 (&w)[NT], float (&sum)[NT], float scale,
+                              const float (&m)[NT]) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float p[8];
+    sum[t] = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       p[e] = __builtin_amdgcn_exp2f(fmaf(z[t][e / 4][e % 4], scale, -m[t]));
-      l[t] += p[e];
+      sum[t] += p[e];
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[t][e] = pack2<E>(p[2 * e], p[2 * e + 1]);
   }
+}
+template <typename E, bool kEdge, int NT, int kN>
+__device__ inline void weigh(f32x4 (&z)[NT][2], u32x4 (&w)[NT], float scale, int key, const int (&lim)[NT],
+                             float (&m)[NT], float (&l)[NT], f32x4 (&o)[NT][kN]) {
+  float top[NT], sum[NT];
+  if (look_up<kEdge>(z, top, scale, key, lim, m)) follow(top, m, l, o);
+  powers<E>(z, w, sum, scale, m);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) l[t] += sum[t];
 }
 
 // Values of 32 keys meet the weights, 16 dimensions at a time; values(i) has them.
@@ -218,6 +235,11 @@ __device__ inline void mix_slowly(const uint16_t* values, const u32x4 (&w)[NT], 
       }
   }
 }
+
+template <int N>
+struct Count { static constexpr int value = N; };
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 
 // A stretch of a set's keys, for one key head: where the pages' parts of it stand.
 struct Stretch {
@@ -288,28 +310,31 @@ __device__ inline void narrow_set(const AttendArgs& a, const AttendSet& set, con
 #pragma unroll
     for (int i = 0; i < kN; ++i) o[t][i] = f32x4{0, 0, 0, 0};
   }
-  for (; key < keys.hi; key += kStep) {
-    const bool edge = key + 32 > set.base + 1;  // some row does not see all keys
-    const bool more = key + kStep < keys.hi;
-    f32x4 z[NT][2];
-    u32x4 w[NT];
+  // the tiles that every row sees whole, then the others: a loop each, so that the
+  // first has the registers to itself
+  const auto pass = [&](auto edge, int end) {
+    for (; key < end; key += kStep) {
+      const bool more = key + kStep < keys.hi;
+      f32x4 z[NT][2];
+      u32x4 w[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) score<E>(kf[h], q[t], z[t][h]);
-    if (more) bring_keys(next, key + kStep);
-    if (!edge) {
-      weigh<E, false>(z, w, a.scale, key + g * 8, lim, m, l, o);
-      mix<E>([&](int i) { return vf[i]; }, w, o);
-    } else {
-      weigh<E, true>(z, w, a.scale, key + g * 8, lim, m, l, o);
-      if (!mix_edge<E>([&](int i) { return vf[i]; }, w, key, set.key1, o))
+        for (int h = 0; h < 2; ++h) score<E>(kf[h], q[t], z[t][h]);
+      if (more) bring_keys(next, key + kStep);
+      weigh<E, decltype(edge)::value>(z, w, a.scale, key + g * 8, lim, m, l, o);
+      const auto values = [&](int i) { return vf[i]; };
+      if constexpr (!decltype(edge)::value)
+        mix<E>(values, w, o);
+      else if (!mix_edge<E>(values, w, key, set.key1, o))
         mix_slowly<E>((const uint16_t*)(c.v + keys.at(c, page, key)), w, key, set.key1, lim, o);
+      if (more) bring_values(next, key + kStep);
+      page = next;
+      next = keys.page(c, key + 2 * kStep);
     }
-    if (more) bring_values(next, key + kStep);
-    page = next;
-    next = keys.page(c, key + 2 * kStep);
-  }
+  };
+  pass(No{}, min(keys.hi, set.base - 30));  // key + 32 <= base + 1
+  pass(Yes{}, keys.hi);
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     l[t] += lane_xor<16>(l[t]);
@@ -371,6 +396,60 @@ __global__ __launch_bounds__(kThreads) void k_attend(AttendArgs a) {
   }
 }
 
+// The wide sets' inner loop: one tile's values meet its weights w while the next tile's
+// scores are taken and become weights, in an order laid down here step by step (the
+// compiler would put the products and the exponentials one after the other): eight
+// steps a row tile, in each a product or two of the matrix unit and an eighth of the
+// vector unit's work for the row tile whose scores are ready.
+template <typename E, int kC, int kN, int NT>
+__device__ inline void in_turn(const u32x4 (*keys)[kWave], const u32x4 (*values)[kWave], const u32x4 (&q)[NT][kC],
+                               u32x4 (&w)[NT], f32x4 (&o)[NT][kN], f32x4 (&z)[NT][2], float (&top)[NT],
+                               float (&sum)[NT], float scale, const float (&m)[NT]) {
+  const int lane = threadIdx.x % kWave;
+  float before[NT];
+  u32x4 w_next[NT];
+  const auto weigh_one = [&](int t, int e) {  // score e of row tile t
+    const float x = z[t][e / 4][e % 4], p = __builtin_amdgcn_exp2f(fmaf(x, scale, -m[t]));
+    top[t] = e ? fmaxf(top[t], x) : x;
+    sum[t] = e ? sum[t] + p : p;
+    if (e % 2) w_next[t][e / 2] = pack2<E>(before[t], p);
+    else before[t] = p;
+  };
+  constexpr int kAhead = 2;
+  u32x4 kf[2 * kC], vf[kN];  // a few of each live
+#pragma unroll
+  for (int t = 0; t < NT; ++t) z[t][0] = z[t][1] = f32x4{0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) kf[j] = keys[j % 2 * kC + j / 2][lane];
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int j = 0; j < 2 * kC; ++j) {
+    const int n = j + kAhead;
+    if (n < 2 * kC) kf[n] = keys[n % 2 * kC + n / 2][lane];
+    else if (n - 2 * kC < kAhead) vf[n - 2 * kC] = values[n - 2 * kC][lane];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) z[t][j % 2] = E::mfma(kf[j], q[t][j / 2], z[t][j % 2]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    if (i + kAhead < kN) vf[i + kAhead] = values[i + kAhead][lane];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      o[t][i] = E::mfma(vf[i], w[t], o[t][i]);
+#pragma unroll
+      for (int e = i * 8 / kN; e < (i + 1) * 8 / kN; ++e) weigh_one(t, e);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  // here, not where they turn out to be needed
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    asm volatile("" : "+v"(w_next[t]), "+v"(sum[t]));
+    w[t] = w_next[t];
+  }
+}
+
 // A workgroup goes over a piece of the wide line: its waves share the set's tiles of
 // 16 rows, NT each, and a tile of keys and values stands in LDS, brought there past the
 // registers while the one before it is in use.  Two workgroups a CU, so that one's
@@ -380,50 +459,47 @@ __device__ inline void to_lds(const char* from, void* to) {  // 16 bytes a lane,
                                    (__attribute__((address_space(3))) void*)to, 16, 0, 0);
 }
 template <typename E, int D, int NT>
-__global__ __launch_bounds__(kThreads, 2) void k_attend_wide(AttendArgs a) {
+__global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void k_attend_wide(AttendArgs a) {
   constexpr int kC = D / 32, kN = D / 16, kF = 2 * kC + kN;  // KiB of 32 keys
-  constexpr int kU = D > 128 ? 1 : 2, kKeys = 32 * kU;       // of a tile
-  __shared__ u32x4 tile[2][kU][kF][kWave];
+  constexpr int kRing = 4;                                   // tiles of 32 keys
+  __shared__ u32x4 tile[kRing][kF][kWave];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
   const int col = lane % 16, g = lane / 16;
   const CacheView& c = a.c;
+  const int no_limit[NT] = {};
   Cursor at;
   if (!begin(a, kWide, at)) return;
   while (at.x < at.end) {
     const AttendSet set = a.p.sets[kWide][at.s];
-    const int nb = set.blocks();
-    const int cnt = (int)min((int64_t)(nb - at.blk), at.end - at.x);
+    const int cnt = (int)min((int64_t)(set.blocks() - at.blk), at.end - at.x);
     const Stretch keys = stretch(a, set, at.head, at.blk, cnt);
-    int page[kU];  // of the tile to bring next
-    const auto look = [&](int key) {
+    const int tiles = (keys.hi - keys.lo + 31) / 32;
+    int page = keys.page(c, keys.lo);  // of the tile to bring next
+    const auto bring = [&](int i) {
+      if (i >= tiles) return;
+      const int64_t from = keys.at(c, page, keys.lo + 32 * i) + lane * 16;
+      page = keys.page(c, keys.lo + 32 * i + 32);
+      static_assert(kF % kWaves == 0, "a tile in equal parts");
 #pragma unroll
-      for (int u = 0; u < kU; ++u) page[u] = keys.page(c, key + 32 * u);
-    };
-    const auto bring = [&](int key, int stage) {
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (key + 32 * u >= keys.hi) break;
-        const int64_t from = keys.at(c, page[u], key + 32 * u) + lane * 16;
-#pragma unroll
-        for (int i = 0; i < kF / kWaves; ++i) {
-          const int f = i * kWaves + wave;
-          to_lds(f < 2 * kC ? c.k + from + f * 1024 : c.v + from + (f - 2 * kC) * 1024, &tile[stage][u][f][0]);
-        }
+      for (int k = 0; k < kF / kWaves; ++k) {
+        const int f = k * kWaves + wave;
+        to_lds(f < 2 * kC ? c.k + from + f * 1024 : c.v + from + (f - 2 * kC) * 1024, &tile[i % kRing][f][0]);
       }
     };
-    static_assert(kF % kWaves == 0, "a tile in equal parts");
-    look(keys.lo);
+    const auto arrived = [&](bool all) {  // the tiles but the last one on its way, for every wave
+      if (all) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      else asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kF / kWaves) : "memory");
+      __syncthreads();
+    };
     __syncthreads();  // the last set's tiles are done with
-    bring(keys.lo, 0);
-    look(keys.lo + kKeys);
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) bring(i);
     u32x4 q[NT][kC];
-    int lim[NT];
     f32x4 o[NT][kN];
     float m[NT], l[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const Row row = row_at(a, set, at.head, (t * kWaves + wave) * 16 + col);
-      lim[t] = row.lim;
 #pragma unroll
       for (int i = 0; i < kC; ++i)
         q[t][i] = row.q >= 0 ? *(const u32x4*)(a.q + 2 * (row.q + i * 32 + g * 8)) : u32x4{0, 0, 0, 0};
@@ -431,53 +507,56 @@ __global__ __launch_bounds__(kThreads, 2) void k_attend_wide(AttendArgs a) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) o[t][i] = f32x4{0, 0, 0, 0};
     }
-    int stage = 0;
-    for (int key = keys.lo; key < keys.hi; key += kKeys, stage ^= 1) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();  // every wave's part of the tile is there, and the tile before done with
-      if (key + kKeys < keys.hi) bring(key + kKeys, stage ^ 1);
-      look(key + 2 * kKeys);
-      const bool edge = key + kKeys > set.base + 1;  // some row does not see all keys
+    // one tile's values and the next one's scores and weights go side by side; where a
+    // row's m has to follow, which is rare, the inner loop is left for it
+    u32x4 w[NT];
+    f32x4 z[NT][2];
+    float top[NT], sum[NT];  // of the tile whose weights are in w: not yet in l
+    arrived(true);
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        f32x4 z[NT][2];
-        u32x4 w[NT];
+    for (int h = 0; h < 2; ++h) {
+      u32x4 kf[kC];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          u32x4 kf[kC];
+      for (int j = 0; j < kC; ++j) kf[j] = tile[0][h * kC + j][lane];
 #pragma unroll
-          for (int i = 0; i < kC; ++i) kf[i] = tile[stage][u][h * kC + i][lane];
-#pragma unroll
-          for (int t = 0; t < NT; ++t) score<E>(kf, q[t], z[t][h]);
-        }
-        const int key32 = key + 32 * u;
-        const auto values = [&](int i) { return tile[stage][u][2 * kC + i][lane]; };
-        if (!edge) {
-          weigh<E, false>(z, w, a.scale, 0, lim, m, l, o);
-          mix<E>(values, w, o);
-        } else if (key32 < keys.hi) {
-          weigh<E, true>(z, w, a.scale, key32 + g * 8, lim, m, l, o);
-          if (!mix_edge<E>(values, w, key32, set.key1, o))
-            mix_slowly<E>((const uint16_t*)&tile[stage][u][2 * kC], w, key32, set.key1, lim, o);
-        }
-      }
+      for (int t = 0; t < NT; ++t) score<E>(kf, q[t], z[t][h]);
     }
+    look_up<false>(z, top, a.scale, 0, no_limit, m);
+    bool far = true;
+    for (int i = 0;;) {
+      if (far) {
+        follow(top, m, l, o);
+        powers<E>(z, w, sum, a.scale, m);
+      }
+      if (i + 1 == tiles) break;
+      do {
+        arrived(i + 2 >= tiles);
+        bring(i + kRing - 1);  // in place of the tile before this one
+#pragma unroll
+        for (int t = 0; t < NT; ++t) l[t] += sum[t];
+        in_turn<E>(&tile[(i + 1) % kRing][0], &tile[i % kRing][2 * kC], q, w, o, z, top, sum, a.scale, m);
+        far = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) far |= (top[t] *= a.scale) > m[t] + kSlack;
+        far = __any(far);
+        ++i;
+      } while (!far && i + 1 < tiles);
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) l[t] += sum[t];
+    const u32x4(*last)[kWave] = &tile[(tiles - 1) % kRing][2 * kC];
+    mix<E>([&](int j) { return last[j][lane]; }, w, o);
     const int64_t part = at.part();
-    const bool whole = set.alone && cnt == nb;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       l[t] += lane_xor<16>(l[t]);
       l[t] += lane_xor<32>(l[t]);
       const int j = (t * kWaves + wave) * 16 + col;
       if (j >= set.n) continue;
-      const float norm = 1.0f / l[t];
-      char* out = a.out + 2 * (whole ? row_at(a, set, at.head, j).out : 0);
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        if (whole) put4<E>(out + 2 * (i * 16 + g * 4), o[t][i], norm);
-        else *(f32x4*)(a.part_o[kWide] + (part * a.rows[kWide] + j) * D + i * 16 + g * 4) = o[t][i];
-      }
-      if (!whole && g == 0) *(f32x2*)(a.part_ml[kWide] + (part * a.rows[kWide] + j) * 2) = f32x2{m[t], l[t]};
+      for (int i = 0; i < kN; ++i)
+        *(f32x4*)(a.part_o[kWide] + (part * a.rows[kWide] + j) * D + i * 16 + g * 4) = o[t][i];
+      if (g == 0) *(f32x2*)(a.part_ml[kWide] + (part * a.rows[kWide] + j) * 2) = f32x2{m[t], l[t]};
     }
     advance(at, cnt);
   }
@@ -489,98 +568,92 @@ __device__ inline int piece_of(int64_t x, int64_t total, int64_t piece) {
   return total >> 32 ? (int)(x / piece) : (int)((uint32_t)x / (uint32_t)piece);
 }
 
-// Joins the partial results of every row; a wave a row and head.  NaN where the
-// session failed.  The parts' weights come first, a lane a part, so that the loads of
-// their values do not wait for one another.
+// Joins the partial results of every row.  A lane has 8 dimensions of a row and head, a
+// wave some heads of a row, side by side; parts are loaded several at a time, as what
+// they wait for is memory.  NaN where the session failed.
+template <int D>
+struct Join {
+  static constexpr int kLanes = D == 96 ? 16 : D / 8;         // of a row and head
+  static constexpr int kHeads = kWaves * kWave / kLanes;      // of a workgroup
+};
 template <typename E, int D>
 __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a) {
-  constexpr int kVec = D % 128 == 0 ? D / 64 : D == 96 ? 2 : 1;  // elements a lane
-  const int lane = threadIdx.x % kWave;
+  constexpr int kLanes = Join<D>::kLanes;
   const CacheView& c = a.c;
   const int b = blockIdx.x / a.R, r = blockIdx.x % a.R;
-  const int heads = a.G * c.n_kv, hq = blockIdx.y * kWaves + threadIdx.x / kWave;
+  const int heads = a.G * c.n_kv, hq = blockIdx.y * Join<D>::kHeads + threadIdx.x / kLanes;
+  const int d = threadIdx.x % kLanes * 8;
   const AttendSession ss = a.p.sess[b];
   const AttendHead lines = *a.p.head;
-  if (hq >= heads || (ss.status == 0 && r >= ss.n)) return;
-  const bool mine = lane * kVec < D;
-  float o[kVec], m = kLowest, l = ss.status == 0 ? 0 : NAN;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) o[i] = 0;
+  if (hq >= heads || d >= D || (ss.status == 0 && r >= ss.n)) return;
+  f32x4 o[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+  float m = kLowest, l = ss.status == 0 ? 0 : NAN;
   if (ss.status == 0) {
     const int head = hq / a.G;
 #pragma unroll
-    for (int level = 0; level < 3; ++level) {
+    for (int level = 0; level < kKinds; ++level) {
       if (ss.first[level] < 0) continue;
       const int first = ss.first[level] / 2, line = ss.first[level] % 2;
-      const AttendSet* sets = a.p.sets[line];
+      const AttendSet& set = a.p.sets[line][first];
       // a session's own sets begin with its first row, a run's with the run's
-      const int t0 = level < 2 ? sets[first].t0 : ss.t0;
-      const int per = sets[first].per;
-      const int j = (ss.t0 + r - t0) * a.G + hq % a.G;
-      const int s = first + j / per, row = j % per;
-      const int nb = sets[first].blocks();
+      const int j = (ss.t0 + r - set.t0) * a.G + hq % a.G, nth = j / set.per, row = j - nth * set.per;
+      const int nb = set.blocks();
       const int64_t blocks = line ? lines.blocks[1] : lines.blocks[0];
-      const int64_t x = head * blocks + sets[first].cum + (int64_t)(j / per) * nb;
       const int64_t total = line ? lines.total[1] : lines.total[0];
       const int64_t piece = line ? lines.piece[1] : lines.piece[0];
-      const int p0 = piece_of(x, total, piece), parts = piece_of(x + nb - 1, total, piece) - p0 + 1;
-      if (parts == 1 && sets[first].alone) return;
+      const int64_t x = head * blocks + set.cum + (int64_t)nth * nb;
+      const int p0 = piece_of(x, total, piece), n = piece_of(x + nb - 1, total, piece) - p0 + 1;
+      if (n == 1 && set.alone) return;
       const int rows = line ? a.rows[1] : a.rows[0];
-      const float* part_ml = line ? a.part_ml[1] : a.part_ml[0];
-      const float* part_o = line ? a.part_o[1] : a.part_o[0];
       const int n_sets = line ? lines.sets[1] : lines.sets[0];
-      const int64_t at = ((int64_t)head * n_sets + s + p0) * rows + row;
-      for (int i0 = 0; i0 < parts; i0 += kWave) {
-        const int n = min(parts - i0, kWave);
-        f32x2 ml = {kLowest, 0};
-        if (lane < n) ml = *(const f32x2*)(part_ml + (at + (int64_t)(i0 + lane) * rows) * 2);
-        const float now = fmaxf(m, wave_reduce(ml[0], OpMax()));
-        const float old = __builtin_amdgcn_exp2f(m - now), w = __builtin_amdgcn_exp2f(ml[0] - now);
-        m = now;
-        l = l * old + wave_reduce(ml[1] * w, OpAdd());
+      const int64_t at = ((int64_t)head * n_sets + first + nth + p0) * rows + row;
+      const float* part_ml = (line ? a.part_ml[1] : a.part_ml[0]) + at * 2;
+      const float* part_o = (line ? a.part_o[1] : a.part_o[0]) + at * D + d;
+      const auto take = [&](auto step, int k0) {
+        constexpr int kStep = decltype(step)::value;
+        f32x2 ml[kStep];
+        f32x4 y[kStep][2];
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) o[i] *= old;
-        const float* y = part_o + (at + (int64_t)i0 * rows) * D + (mine ? lane * kVec : 0);
-        constexpr int kStep = 8;
-        for (int k0 = 0; k0 < n; k0 += kStep) {
-          float v[kStep][kVec];
-#pragma unroll
-          for (int k = 0; k < kStep; ++k)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) v[k][i] = y[(int64_t)min(k0 + k, n - 1) * rows * D + i];
-#pragma unroll
-          for (int k = 0; k < kStep; ++k) {
-            const float wk = lane_read(w, min(k0 + k, n - 1));
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) o[i] = k0 + k < n ? fmaf(v[k][i], wk, o[i]) : o[i];
-          }
+        for (int k = 0; k < kStep; ++k) {
+          const int64_t to = (int64_t)min(k0 + k, n - 1) * rows;
+          ml[k] = *(const f32x2*)(part_ml + to * 2);
+          y[k][0] = *(const f32x4*)(part_o + to * D);
+          y[k][1] = *(const f32x4*)(part_o + to * D + 4);
         }
-      }
+        float now = m;
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) now = fmaxf(now, ml[k][0]);
+        const float old = __builtin_amdgcn_exp2f(m - now);
+        m = now;
+        l *= old, o[0] *= old, o[1] *= old;
+#pragma unroll
+        for (int k = 0; k < kStep; ++k) {
+          const float w = __builtin_amdgcn_exp2f(ml[k][0] - now);
+          if (k0 + k < n) l += ml[k][1] * w, o[0] += y[k][0] * w, o[1] += y[k][1] * w;
+        }
+      };
+      if (n <= 2) take(Count<2>{}, 0);
+      else for (int k0 = 0; k0 < n; k0 += 8) take(Count<8>{}, k0);
     }
   }
-  if (!mine) return;
-  char* out = a.out + 2 * (((int64_t)blockIdx.x * heads + hq) * D + lane * kVec);
   const float norm = 1.0f / l;
-  if constexpr (kVec == 1) {
-    *(uint16_t*)out = (uint16_t)pack2<E>(o[0] * norm, 0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kVec; i += 2) *(uint32_t*)(out + 2 * i) = pack2<E>(o[i] * norm, o[i + 1] * norm);
-  }
+  char* out = a.out + 2 * (((int64_t)blockIdx.x * heads + hq) * D + d);
+  *(u32x4*)out = u32x4{pack2<E>(o[0][0] * norm, o[0][1] * norm), pack2<E>(o[0][2] * norm, o[0][3] * norm),
+                       pack2<E>(o[1][0] * norm, o[1][1] * norm), pack2<E>(o[1][2] * norm, o[1][3] * norm)};
 }
 
 template <typename E, int D>
 void launch(const AttendArgs& a, hipStream_t st) {
   // rows that neighbours share go together, which may make them many
   if (a.B > 1 || a.R * a.G > a.rows[kNarrow])
-    hipLaunchKernelGGL((k_attend_wide<E, D, wide_tiles(D)>), dim3(kPieces), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((k_attend_wide<E, D, wide_tiles(D)>), dim3(kPieces[kWide]), dim3(kThreads), 0, st, a);
   if (a.rows[kNarrow] == 16)
-    hipLaunchKernelGGL((k_attend<E, D, 1>), dim3(kPieces), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((k_attend<E, D, 1>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
   else if (a.rows[kNarrow] == 32)
-    hipLaunchKernelGGL((k_attend<E, D, 2>), dim3(kPieces), dim3(kThreads), 0, st, a);
+    hipLaunchKernelGGL((k_attend<E, D, 2>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
   else if constexpr (D <= 128)
-    hipLaunchKernelGGL((k_attend<E, D, 4>), dim3(kPieces), dim3(kThreads), 0, st, a);
-  const unsigned gy = (a.G * a.c.n_kv + kWaves - 1) / kWaves;
+    hipLaunchKernelGGL((k_attend<E, D, 4>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
+  const unsigned gy = (a.G * a.c.n_kv + Join<D>::kHeads - 1) / Join<D>::kHeads;
   hipLaunchKernelGGL((k_join<E, D>), dim3(a.B * a.R, gy), dim3(kThreads), 0, st, a);
 }
 template <typename E>
@@ -606,7 +679,7 @@ Parts parts_of(const sv_cache* c, const PlanSizes& z, int32_t R, int32_t G) {
   p.rows[kWide] = wide_rows(c->head_dim);
   p.bytes = 0;
   for (int line = 0; line < 2; ++line) {
-    p.slots[line] = z.sets[line] * c->n_kv + kPieces;
+    p.slots[line] = z.sets[line] * c->n_kv + kPieces[line];
     p.bytes += p.slots[line] * p.rows[line] * (c->head_dim + 2) * 4;
   }
   return p;

@@ -6,7 +6,8 @@
 // that it has alone, or rows of neighbouring sessions over keys that they share.
 // Where they fit one wave's registers the set is narrow: the waves of a workgroup
 // take its keys in turn, and what counts is the bytes that arrive.  Else it is
-// wide: the waves take its rows, and share the keys in LDS.  Keys are counted in
+// wide: the waves take its rows, and share the keys in LDS; every row of a wide set
+// sees all of its keys, what rows see in part is left to narrow ones.  Keys are counted in
 // blocks of kBlock.  The narrow sets' blocks stand in one line, the first key head's,
 // then the second's and so on, the wide sets' in another; a line is cut into equal
 // pieces, a piece a workgroup.  Piece i leaves a partial result (largest score, sum,
@@ -23,7 +24,7 @@ namespace sv {
 
 constexpr int kBlock = 128;     // keys
 constexpr int kNarrow = 0, kWide = 1;
-constexpr int kPieces = 512;    // of a line at most: two a CU
+constexpr int kPieces[2] = {512, 512};  // of a line: two workgroups a CU, and one
 constexpr int kFar = 1 << 30;   // no limit on keys
 
 struct AttendSet {
@@ -42,11 +43,13 @@ struct AttendSet {
 static_assert(sizeof(AttendSet) == 48, "AttendSet layout");
 
 // A session's rows stand in the sets from first[0] (its run's shared keys), first[1]
-// (its run's in that run) and first[2] (its own keys) on: 2 * set + line, -1: none.
+// (its run's in that run), first[2] (its own keys that all its rows see, where these
+// are many) and first[3] (its other keys) on: 2 * set + line, -1: none.
+constexpr int kKinds = 4;
 struct AttendSession {
   int32_t status, n, t0;  // rows in use, their first place in row_of
-  int32_t first[3];
-  int32_t pad[2];
+  int32_t first[kKinds];
+  int32_t pad;
 };
 
 struct AttendHead {
@@ -57,7 +60,7 @@ struct AttendHead {
 struct AttendPlan {
   AttendHead* head;
   AttendSession* sess;   // [B]
-  int4* starts[2];       // [kPieces]: set, key head, block; of pieces that begin before total
+  int4* starts[2];       // a piece: set, key head, block; of pieces that begin before total
   int32_t* shared;       // [B]: keys shared with the session before
   int32_t* row_of;       // [B * R]: session * R + round row
   AttendSet* sets[2];
@@ -81,9 +84,10 @@ inline PlanSizes plan_sizes(int32_t B, int32_t R, int32_t G, int32_t head_dim) {
   PlanSizes z;
   const int64_t rows = (int64_t)R * G, wide = wide_rows(head_dim);
   const int64_t runs = 2 * ((int64_t)B / 2 + 1);  // of two sessions or more, on two levels
-  z.sets[kNarrow] = B + runs;
+  const int64_t narrow = narrow_rows(rows, head_dim);
+  z.sets[kNarrow] = B * ((rows + narrow - 1) / narrow) + runs;
   z.sets[kWide] = 2 * ((B * rows + wide - 1) / wide) + runs;
-  if (rows > narrow_rows(rows, head_dim)) z.sets[kWide] += B * ((rows + wide - 1) / wide);
+  if (rows > narrow) z.sets[kWide] += B * ((rows + wide - 1) / wide);
   int64_t at = 256;
   const auto take = [&at](int64_t n) {
     const int64_t here = at;
@@ -91,7 +95,7 @@ inline PlanSizes plan_sizes(int32_t B, int32_t R, int32_t G, int32_t head_dim) {
     return here;
   };
   z.sess = take((int64_t)B * sizeof(AttendSession));
-  z.starts = take(2 * kPieces * sizeof(int4));
+  z.starts = take((kPieces[0] + kPieces[1]) * sizeof(int4));
   z.shared = take((int64_t)B * 4);
   z.row_of = take((int64_t)B * R * 4);
   for (int line = 0; line < 2; ++line) z.set_at[line] = take(z.sets[line] * sizeof(AttendSet));
@@ -101,7 +105,7 @@ inline PlanSizes plan_sizes(int32_t B, int32_t R, int32_t G, int32_t head_dim) {
 inline AttendPlan plan_of(const PlanSizes& z, void* p) {
   char* c = (char*)p;
   int4* starts = (int4*)(c + z.starts);
-  return AttendPlan{(AttendHead*)c, (AttendSession*)(c + z.sess), {starts, starts + kPieces},
+  return AttendPlan{(AttendHead*)c, (AttendSession*)(c + z.sess), {starts, starts + kPieces[0]},
                     (int32_t*)(c + z.shared), (int32_t*)(c + z.row_of),
                     {(AttendSet*)(c + z.set_at[0]), (AttendSet*)(c + z.set_at[1])}};
 }

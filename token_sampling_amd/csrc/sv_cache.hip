@@ -10,7 +10,6 @@ namespace sv {
 namespace {
 
 constexpr int kOne = 1024;                          // threads of the single workgroups
-constexpr int kPer = SV_CACHE_B_MAX / kOne;         // sessions a thread
 constexpr int kTile = 32 * kOne;                    // pages looked at together
 
 struct Pair {
@@ -82,7 +81,9 @@ struct ReserveArgs {
   int32_t B;
 };
 
-// One workgroup: what the sessions want, the free pages, and who gets which.
+// One workgroup, kPer sessions a thread: what the sessions want, the free pages, and
+// who gets which.
+template <int kPer>
 __global__ __launch_bounds__(kOne) void k_reserve(ReserveArgs a) {
   __shared__ uint32_t seen[SV_CACHE_SLOTS_MAX / 32], twice[SV_CACHE_SLOTS_MAX / 32];
   __shared__ int64_t smem[kOne / kWave];
@@ -458,7 +459,8 @@ extern "C" int sv_cache_reserve(const sv_cache* cache, const int32_t* slots, con
   (void)hipGetLastError();
   const Scratch s = scratch_of(cache, B, workspace);
   const ReserveArgs a = {view_of(cache), s, slots, add, status, B};
-  hipLaunchKernelGGL(k_reserve, dim3(1), dim3(kOne), 0, st, a);
+  if (B <= kOne) hipLaunchKernelGGL(k_reserve<1>, dim3(1), dim3(kOne), 0, st, a);
+  else hipLaunchKernelGGL(k_reserve<SV_CACHE_B_MAX / kOne>, dim3(1), dim3(kOne), 0, st, a);
   const CopyArgs p = {a.c, s.n_pairs, s.pairs, nullptr, nullptr};
   const int64_t units = (int64_t)B * 2 * cache->n_layers;
   hipLaunchKernelGGL(k_copy, dim3((unsigned)(units < 2048 ? units : 2048)), dim3(kCopy), 0, st, p);

@@ -6,7 +6,6 @@ namespace sv {
 namespace {
 
 constexpr int kOne = 1024;
-constexpr int kPer = SV_CACHE_B_MAX / kOne;
 constexpr int kNone = 0x7FFFFFFF;
 
 struct PlanArgs {
@@ -69,6 +68,14 @@ __device__ inline Cut cut_rows(const PlanArgs& a, int64_t rows) {
   return Cut{kWide, n, (int)((rows + n - 1) / n + 15) / 16 * 16};
 }
 
+// The keys of a session's own, behind the `from` that it shares: where those end that
+// go into wide sets (whole blocks that all rows see, where the rows are many).
+__device__ inline int clear_end(const PlanArgs& a, int rows, int len, int from) {
+  return (int64_t)rows * a.G > a.narrow ? max(from, len / kBlock * kBlock) : from;
+}
+
+// One workgroup, kPer sessions a thread.
+template <int kPer>
 __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
   // by session: the first row's place; in each line the first set, and the blocks
   // before it
@@ -126,10 +133,12 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
     int64_t total;
     const int64_t t = rows_all + block_incl_scan<kOne, int64_t>(n[i], smem, total) - n[i];
     if (b < a.B) t_at[b] = (int)t;
-    for (int r = 0; r < n[i]; ++r) a.p.row_of[t + r] = b * a.R + r;
     rows_all += total;
   }
   if (tid == 0) t_at[a.B] = (int)rows_all;
+  __syncthreads();
+  for (int b = tid / kWave; b < a.B; b += kOne / kWave)  // a wave a session
+    for (int r = tid % kWave; r < t_at[b + 1] - t_at[b]; r += kWave) a.p.row_of[t_at[b] + r] = b * a.R + r;
 
   // runs of sessions that share their first keys; in them, runs that share more
 #pragma unroll
@@ -157,8 +166,8 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
   }
 
   // every session's sets: its runs' where they begin with it, then its own
-  Cut cut[3][kPer];
-  int key[3][kPer];            // where the keys of the three end
+  Cut cut[kKinds][kPer];
+  int key[kKinds][kPer];  // where their keys end
   int64_t cum[2][kPer], sets_all[2] = {0, 0}, cum_all[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -166,20 +175,23 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
     const int b = i * kOne + tid;
     int64_t sets[2] = {0, 0}, blocks[2] = {0, 0};
 #pragma unroll
-    for (int k = 0; k < 3; ++k) cut[k][i] = Cut{0, 0, 16}, key[k][i] = 0;
+    for (int k = 0; k < kKinds; ++k) cut[k][i] = Cut{0, 0, 16}, key[k][i] = 0;
     if (b < a.B) {
       int from = 0;
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
+      for (int k = 0; k < kKinds; ++k) {
         bool begins = true;
         if (k < 2) {
           const int r = run[k][i], d = depth[k][r] == kNone ? from : depth[k][r];
           key[k][i] = d;
           if (d > from) cut[k][i] = cut_rows(a, (int64_t)(t_at[first[k][r + 1]] - t_at[first[k][r]]) * a.G);
           begins = first[k][r] == b;
+        } else if (k == 2) {
+          key[k][i] = clear_end(a, n[i], len[i], from);
+          if (key[k][i] > from) cut[k][i] = cut_rows(a, (int64_t)n[i] * a.G);
         } else {
           key[k][i] = len[i] + n[i];
-          cut[k][i] = cut_rows(a, (int64_t)n[i] * a.G);
+          cut[k][i] = Cut{kNarrow, (n[i] * a.G + a.narrow - 1) / a.narrow, a.narrow};
         }
         if (begins && cut[k][i].n > 0) {
           const int64_t nb = (key[k][i] - from + kBlock - 1) / kBlock;
@@ -206,12 +218,12 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
     if (i * kOne >= a.B) break;
     const int b = i * kOne + tid;
     if (b >= a.B) continue;
-    AttendSession ss = {st[i], n[i], t_at[b], {-1, -1, -1}, {0, 0}};
+    AttendSession ss = {st[i], n[i], t_at[b], {-1, -1, -1, -1}, 0};
     int s[2] = {set_at[0][b], set_at[1][b]};
     int64_t x[2] = {cum[0][i], cum[1][i]};
     int from = 0;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < kKinds; ++k) {
       const Cut& cc = cut[k][i];
       const int f = k < 2 ? first[k][run[k][i]] : b;
       if (cc.n > 0) {
@@ -225,7 +237,7 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
           if (n[i] > 0 || k < 2) ss.first[k] = 2 * at + cc.line;
           for (int q = 0; q < cc.n; ++q, ++at, y += nb)
             a.p.sets[cc.line][at] = AttendSet{t_at[b], q * cc.per, min(cc.per, rows - q * cc.per), from,
-                                              key[k][i], list, k < 2 ? kFar : len[i], k == 2 && from == 0,
+                                              key[k][i], list, k < 3 ? kFar : len[i], k == 3 && from == 0,
                                               y, cc.per, 0};
           if (cc.line) s[1] = at, x[1] = y;
           else s[0] = at, x[0] = y;
@@ -239,7 +251,7 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
       }
       from = key[k][i];
     }
-    if (n[i] == 0) ss.first[0] = ss.first[1] = ss.first[2] = -1;
+    if (n[i] == 0) ss.first[0] = ss.first[1] = -1;
     a.p.sess[b] = ss;
     if (a.status) a.status[b] = st[i];
   }
@@ -312,8 +324,9 @@ extern "C" int sv_cache_plan(const sv_cache* cache, const int32_t* slots, const 
   (void)hipGetLastError();
   const PlanArgs a = {view_of(cache), plan_of(z, plan), slots, rows, status, G, B, R,
                       narrow_rows((int64_t)R * G, cache->head_dim), wide_rows(cache->head_dim),
-                      {kPieces, kPieces}, 256};
+                      {kPieces[0], kPieces[1]}, 256};
   hipLaunchKernelGGL(k_shared, dim3(B), dim3(kShared), 0, st, a);
-  hipLaunchKernelGGL(k_plan, dim3(1), dim3(kOne), 0, st, a);
+  if (B <= kOne) hipLaunchKernelGGL(k_plan<1>, dim3(1), dim3(kOne), 0, st, a);
+  else hipLaunchKernelGGL(k_plan<SV_CACHE_B_MAX / kOne>, dim3(1), dim3(kOne), 0, st, a);
   return hipGetLastError() == hipSuccess ? SV_OK : SV_ERR_DEVICE;
 }
