@@ -632,7 +632,7 @@ __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a) {
           if (k0 + k < n) l += ml[k][1] * w, o[0] += y[k][0] * w, o[1] += y[k][1] * w;
         }
       };
-      if (n <= 2) take(Count<2>{}, 0);
+      if (n <= 4) take(Count<4>{}, 0);
       else for (int k0 = 0; k0 < n; k0 += 8) take(Count<8>{}, k0);
     }
   }

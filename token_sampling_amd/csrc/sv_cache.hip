@@ -370,19 +370,31 @@ struct WriteArgs {
 };
 constexpr int kWrite = 256;
 
-// A thread takes 8 dimensions of a head of the up to 8 rows whose positions share
-// an octet of a page: their keys are 16-byte pieces as they come, their values are
-// turned in registers into 8 pieces of 8 tokens.  Pieces of an octet that the rows
-// fill in part are read and written back.
+// A thread takes 8 dimensions of a head of the up to 8 rows whose positions share an
+// octet of a page: the keys of each are a 16-byte piece as it comes, the values are
+// turned in registers into 8 pieces of 8 tokens.  A wave's 512 pieces then change
+// places in LDS, so that it stores them as they lie in the page, keys 64 bytes and
+// values 1 KiB side by side (48 prompts of up to 5000 tokens, 8 heads of 128: stored
+// as they come 345 us).  Pieces of an octet that the rows fill in part are read
+// and written back.
+__device__ inline int64_t shfl64(int64_t x, int lane) {
+  const uint32_t lo = __shfl((int)(uint32_t)x, lane), hi = __shfl((int)(uint32_t)(x >> 32), lane);
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
 __global__ __launch_bounds__(kWrite) void k_write(WriteArgs a) {
+  __shared__ u32x4 pieces[kWrite / kWave][kWave * 8];
   const CacheView& c = a.c;
+  const int lane = threadIdx.x % kWave;
+  u32x4* mine = pieces[threadIdx.x / kWave];
   const int groups = c.n_kv * (c.head_dim / 8);
   const int64_t all = (int64_t)a.octets * (a.offsets ? 1 : a.B) * groups;
-  for (int64_t w = (int64_t)blockIdx.x * kWrite + threadIdx.x; w < all; w += (int64_t)gridDim.x * kWrite) {
+  // whole waves go round, as they work together
+  const int64_t step = (int64_t)gridDim.x * kWrite, waves_end = (all + kWave - 1) / kWave * kWave;
+  for (int64_t w = (int64_t)blockIdx.x * kWrite + threadIdx.x; w < waves_end; w += step) {
     const int64_t item = w / groups;
     const int dg = (int)(w % groups), head = dg / (c.head_dim / 8), d = dg % (c.head_dim / 8) * 8;
-    int b, n, lo = 0, octet;
-    if (a.offsets) {
+    int b = 0, n = 0, lo = 0, octet = 0;
+    if (w < all && a.offsets) {
       // session b's octets are the items from offsets[b] / 8 + 2 b on
       int left = 0, right = a.B - 1;
       while (left < right) {
@@ -394,25 +406,21 @@ __global__ __launch_bounds__(kWrite) void k_write(WriteArgs a) {
       lo = min(max(a.offsets[b], 0), a.R);
       n = min(max(a.offsets[b + 1], 0), a.R) - lo;
       octet = (int)(item - (lo / 8 + 2 * (int64_t)b));
-    } else {
+    } else if (w < all) {
       b = (int)(item / a.octets);
       octet = (int)(item % a.octets);
       n = a.rows ? min(max(a.rows[b], 0), a.R) : a.R;
     }
-    const int h = a.slots ? a.slots[b] : b;
-    if (h < 0 || h >= c.n_slots || n <= 0) continue;
-    const int64_t len = c.lens[h];
+    const int h = n > 0 ? (a.slots ? a.slots[b] : b) : -1;
+    const bool some = h >= 0 && h < c.n_slots;
+    const int64_t len = some ? c.lens[h] : 0;
     const int64_t pos = (len / 8 + octet) * 8;  // the octet's first position
     const int e0 = pos < len ? (int)(len - pos) : 0;
-    const int e1 = (int)min((int64_t)8, len + n - pos);
-    if (len < 0 || e1 <= e0 || pos >> c.shift >= min(c.held[h], c.max_pages)) continue;
-    const int page = c.table[(int64_t)h * c.max_pages + (pos >> c.shift)];
-    if (page < 0 || page >= c.n_pages || c.refs[page] != 1) continue;
-    const int u = (int)(pos & (c.page() - 1));
-    const int64_t at = a.base + page * c.page_elems() + head * c.head_elems();
-    const int64_t row0 = pos - len;  // row of element 0 of the octet (may be < 0)
-    const char* kp = a.k + 2 * (b * a.k_session + (lo + row0) * a.k_row + head * a.k_head + d);
-    const char* vp = a.v + 2 * (b * a.v_session + (lo + row0) * a.v_row + head * a.v_head + d);
+    int e1 = some && len >= 0 ? (int)min((int64_t)8, len + n - pos) : 0;
+    // the rows, which do not wait for the page
+    const int64_t row0 = lo + pos - len;  // row of element 0 of the octet (may lie before the rows)
+    const char* kp = a.k + 2 * (b * a.k_session + row0 * a.k_row + head * a.k_head + d);
+    const char* vp = a.v + 2 * (b * a.v_session + row0 * a.v_row + head * a.v_head + d);
     u32x4 kr[8], vr[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -420,22 +428,62 @@ __global__ __launch_bounds__(kWrite) void k_write(WriteArgs a) {
       kr[e] = in ? *(const u32x4*)(kp + 2 * e * a.k_row) : u32x4{0, 0, 0, 0};
       vr[e] = in ? *(const u32x4*)(vp + 2 * e * a.v_row) : u32x4{0, 0, 0, 0};
     }
+    int page = -1;
+    if (e1 > e0 && pos >> c.shift < min(c.held[h], c.max_pages)) {
+      page = c.table[(int64_t)h * c.max_pages + (pos >> c.shift)];
+      if (page < 0 || page >= c.n_pages || c.refs[page] != 1) page = -1;
+    }
+    if (page < 0) e1 = 0;
+    const int u = (int)(pos & (c.page() - 1));
+    const int64_t at = a.base + max(page, 0) * c.page_elems() + head * c.head_elems();
+    const int64_t k_at = 2 * (at + key_at(u, d, c.head_dim)), v_at = 2 * (at + value_at(u, d, c.head_dim));
+    const int span = e0 | max(e1, 0) << 4;
+    // keys: four tokens of 16 threads at a time; of a thread's pieces the one of token e
+    // stands at place e ^ lane % 8, so that neither side meets in one bank
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e >= e0 && e < e1) *(u32x4*)(c.k + 2 * (at + key_at(u + e, d, c.head_dim))) = kr[e];
-    const bool part = e0 > 0 || e1 < 8;
+    for (int e = 0; e < 8; ++e) mine[lane * 8 + (e ^ lane % 8)] = kr[e];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int from = i / 2 * 16 + lane / 4, e = i % 2 * 4 + lane % 4;
+      const int64_t to = shfl64(k_at, from);
+      const int sp = __shfl(span, from);
+      const u32x4 x = mine[from * 8 + (e ^ from % 8)];
+      if (e >= (sp & 15) && e < sp >> 4)
+        *(u32x4*)(c.k + to + 2 * ((e / 4) * (c.head_dim / 32) * 512 + e % 4 * 8)) = x;
+    }
+    __builtin_amdgcn_wave_barrier();
+    // values
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      u32x4* out = (u32x4*)(c.v + 2 * (at + value_at(u, d + j, c.head_dim)));
-      u32x4 x = part ? *out : u32x4{0, 0, 0, 0};
+      u32x4 x;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t y = vr[e][j / 2] >> (16 * (j % 2)) & 0xFFFFu;
-        const uint32_t put = (x[e / 2] & (0xFFFF0000u >> (16 * (e % 2)))) | y << (16 * (e % 2));
-        x[e / 2] = e >= e0 && e < e1 ? put : x[e / 2];
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x0 = vr[2 * e][j / 2], x1 = vr[2 * e + 1][j / 2];
+        x[e] = j % 2 ? x0 >> 16 | (x1 & 0xFFFF0000u) : (x0 & 0xFFFFu) | x1 << 16;
+      }
+      mine[lane * 8 + (j ^ lane % 8)] = x;
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int from = i * 8 + lane / 8, j = lane % 8;
+      u32x4* out = (u32x4*)(c.v + shfl64(v_at, from) + 16 * j);
+      const int sp = __shfl(span, from), f0 = sp & 15, f1 = sp >> 4;
+      u32x4 x = mine[from * 8 + (j ^ from % 8)];
+      if (f1 <= f0) continue;
+      if (f0 > 0 || f1 < 8) {
+        const u32x4 old = *out;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t mask = (2 * e >= f0 && 2 * e < f1 ? 0xFFFFu : 0u) |
+                                (2 * e + 1 >= f0 && 2 * e + 1 < f1 ? 0xFFFF0000u : 0u);
+          x[e] = (x[e] & mask) | (old[e] & ~mask);
+        }
       }
       *out = x;
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
