@@ -144,7 +144,7 @@ def test_binding_refuses_host_tensors():
     x = torch.zeros((2, 1, 2, 64), dtype=torch.bfloat16)
     for call in (lambda: sv.cache_reserve(c, i), lambda: sv.cache_keep(c, i), lambda: sv.cache_fork(c, i, i),
                  lambda: sv.cache_compact(c), lambda: sv.cache_write(c, 0, x, x), lambda: sv.cache_plan(c, 2, 1, rows=i),
-                 lambda: sv.cache_attention(c, 0, x, sv.CachePlan(i, i, 2, 2, 1))):
+                 lambda: sv.cache_attention(c, 0, x, sv.CachePlan(i, i, 2, 2, 1, 2, 64, 64))):
         with pytest.raises(ValueError):
             call()
 

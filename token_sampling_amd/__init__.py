@@ -178,12 +178,16 @@ class Cache(NamedTuple):
 
 class CachePlan(NamedTuple):
     """How a round's attention is split (cache_plan), for B sessions of up to R rows
-    and n_heads query heads; status [B] int32."""
+    and n_heads query heads over a cache of n_kv heads of head_dim; status [B] int32;
+    workspace_bytes: what cache_attention needs."""
     buffer: "torch.Tensor"  # noqa: F821
     status: "torch.Tensor"  # noqa: F821
     n_heads: int
     B: int
     R: int
+    n_kv: int
+    head_dim: int
+    workspace_bytes: int
 
 
 class HipEvent:
@@ -1039,27 +1043,43 @@ def cache_order(page, head_dim):
 
 
 def _cache_struct(cache, dev):
+    """sv_cache of a Cache; its checks at once where all is as it should be (a round makes
+    a call of this kind in every layer)."""
     import torch
 
-    if cache.k.dtype is torch.bfloat16:
-        dt = BF16
-    elif cache.k.dtype is torch.float16:
-        dt = FP16
+    k, v, table, lens, held, refs = cache
+    try:
+        dtype, int32, i, shape = k.dtype, torch.int32, dev.index, k.shape
+        n_layers, n_pages, n_kv, page, head_dim = shape
+        n_slots, max_pages = table.shape
+        slots = lens.shape
+        good = (v.dtype is dtype and v.shape == shape and table.dtype is int32 and lens.dtype is int32
+                and held.dtype is int32 and refs.dtype is int32 and slots == held.shape
+                and slots[0] == n_slots and len(slots) == 1 and refs.shape == (n_pages,)
+                and k.get_device() == i and v.get_device() == i and table.get_device() == i
+                and lens.get_device() == i and held.get_device() == i and refs.get_device() == i
+                and k.is_contiguous() and v.is_contiguous() and table.is_contiguous()
+                and lens.is_contiguous() and held.is_contiguous() and refs.is_contiguous())
+    except (AttributeError, ValueError, IndexError):
+        good = False
+    if not good:
+        for t, name in zip(cache, Cache._fields):
+            _check(t, f"cache.{name}", torch.int32 if t is not k and t is not v else None, None, dev)
+        if k.dim() != 5 or table.dim() != 2:
+            raise ValueError("cache.k must be [n_layers, n_pages, n_kv, page, head_dim], cache.table "
+                             "[n_slots, max_pages]")
+        _check(v, "cache.v", k.dtype, k.shape, dev)
+        for t, name, n in ((lens, "lens", table.shape[0]), (held, "held", table.shape[0]),
+                           (refs, "refs", k.shape[1])):
+            _check(t, f"cache.{name}", torch.int32, (n,), dev)
+    if dtype is torch.bfloat16:
+        code = BF16
+    elif dtype is torch.float16:
+        code = FP16
     else:
         raise TypeError("caches are bfloat16 or float16")
-    if cache.k.dim() != 5 or cache.table.dim() != 2:
-        raise ValueError("cache.k must be [n_layers, n_pages, n_kv, page, head_dim], cache.table "
-                         "[n_slots, max_pages]")
-    shape = cache.k.shape
-    n_layers, n_pages, n_kv, page, head_dim = shape
-    n_slots, max_pages = cache.table.shape
-    return _Cache(_want(cache.k, "cache.k", cache.k.dtype, shape, dev),
-                  _want(cache.v, "cache.v", cache.k.dtype, shape, dev),
-                  _want(cache.table, "cache.table", torch.int32, (n_slots, max_pages), dev),
-                  _want(cache.lens, "cache.lens", torch.int32, (n_slots,), dev),
-                  _want(cache.held, "cache.held", torch.int32, (n_slots,), dev),
-                  _want(cache.refs, "cache.refs", torch.int32, (n_pages,), dev),
-                  dt, n_layers, n_pages, n_kv, page, head_dim, n_slots, max_pages)
+    return _Cache(k.data_ptr(), v.data_ptr(), table.data_ptr(), lens.data_ptr(), held.data_ptr(),
+                  refs.data_ptr(), code, n_layers, n_pages, n_kv, page, head_dim, n_slots, max_pages)
 
 
 def _cache_slots(cache, slots, B, dev):
@@ -1191,22 +1211,20 @@ def _row_strides(t, name, shape, dtype, dev):
     place do not count."""
     import torch
 
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch tensor")
-    if t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    strides = [s if n > 1 else 0 for s, n in zip(t.stride(), t.shape)]
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index
+            and t.shape == shape):
+        _check(t, name, dtype, shape, dev)
     if t.numel() == 0:
-        return None, [0] * (t.dim() - 1)
-    if strides[-1] != 1:
+        return None, [0] * (len(shape) - 1)
+    strides = [s if n > 1 else 0 for s, n in zip(t.stride(), shape)]
+    if strides.pop() != 1:
         raise ValueError(f"the last axis of {name} must be contiguous")
-    if any(s % 8 for s in strides[:-1]) or t.data_ptr() % 16:
+    address = t.data_ptr()
+    for s in strides:
+        address |= 2 * s
+    if address % 16:
         raise ValueError(f"rows of {name} must begin at multiples of 16 bytes")
-    return t.data_ptr(), strides[:-1]
+    return t.data_ptr(), strides
 
 
 def cache_write(cache, layer, k, v, slots=None, rows=None, offsets=None, stream=None):
@@ -1278,7 +1296,8 @@ def cache_plan(cache, n_heads, R, rows=None, slots=None, B=None, out=None, strea
         rc = lib().sv_cache_plan(ctypes.byref(c), p_slots, p_rows, n_heads, B, R, status.data_ptr(),
                                  buffer.data_ptr(), size, handle)
     _raise(rc, "sv_cache_plan")
-    return CachePlan(buffer, status, n_heads, B, R)
+    return CachePlan(buffer, status, n_heads, B, R, c.n_kv, c.head_dim,
+                     lib().sv_cache_attention_bytes(ctypes.byref(c), n_heads, B, R))
 
 
 def cache_attention(cache, layer, q, plan, scale=None, out=None, workspace=None, stream=None):
@@ -1295,8 +1314,9 @@ def cache_attention(cache, layer, q, plan, scale=None, out=None, workspace=None,
     shape = (B, R, n_heads, c.head_dim)
     p_q, strides = _row_strides(q, "q", shape, cache.k.dtype, dev)
     scale = c.head_dim ** -0.5 if scale is None else float(scale)
-    need = lib().sv_cache_attention_bytes(ctypes.byref(c), n_heads, B, R)
-    _bytes(plan.buffer, lib().sv_cache_plan_bytes(ctypes.byref(c), n_heads, B, R), "plan", dev)
+    if (plan.n_kv, plan.head_dim) != (c.n_kv, c.head_dim):
+        raise ValueError("plan is of a cache of other heads")
+    p_plan = _want(plan.buffer, "plan.buffer", torch.uint8, plan.buffer.shape, dev)
     handle, on = _launch(dev, stream)
     with on:
         if out is None:
@@ -1306,9 +1326,9 @@ def cache_attention(cache, layer, q, plan, scale=None, out=None, workspace=None,
             hi = p_q + 2 * (sum(s * (n - 1) for s, n in zip(strides, shape)) + c.head_dim)
             if out.data_ptr() < hi and p_q < out.data_ptr() + 2 * out.numel():
                 raise ValueError("out overlaps q")
-        workspace, size = _bytes(workspace, need, "workspace", dev)
-        rc = lib().sv_cache_attention(ctypes.byref(c), layer, p_q, *strides, scale,
-                                      plan.buffer.data_ptr(), n_heads, B, R, out.data_ptr(),
+        workspace, size = _bytes(workspace, plan.workspace_bytes, "workspace", dev)
+        rc = lib().sv_cache_attention(ctypes.byref(c), layer, p_q, *strides, scale, p_plan,
+                                      n_heads, B, R, out.data_ptr(),
                                       workspace.data_ptr(), size, handle)
     _raise(rc, "sv_cache_attention")
     return out
