@@ -296,3 +296,24 @@ def test_binding_checks():
     with pytest.raises(sv.SvError):
         sv.cache_attention(cache, 0, q, plan, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     torch.cuda.synchronize()
+
+
+def test_many_sessions_share():
+    """More sessions than a plan's workgroup has threads, behind one prompt, rows of one
+    and of several tokens, a few idle places among them."""
+    rng = np.random.default_rng(13)
+    n, page = 1300, 64
+    cache = sv.make_cache(n + 1, 9 + 2 * n, 8, 1, 64, page=page)
+    sv.cache_reserve(cache, dev([300]), slots=dev([n]))
+    sv.cache_keep(cache, dev([300]), slots=dev([n]))
+    sv.cache_fork(cache, dev([n] * n), dev(range(n)))
+    rows = rng.integers(1, 4, n)
+    assert not sv.cache_reserve(cache, dev(rows), slots=dev(range(n))).any()
+    for x in cache[:2]:
+        x.normal_()
+    from tests.cache_ref import Ref
+    ref = Ref(cache)
+    ref.sound()
+    slots = np.arange(n)
+    slots[rng.random(n) < 0.1] = -1
+    check(cache, ref, slots, rows, queries(rng, (n, 3, 2, 64), torch.bfloat16))

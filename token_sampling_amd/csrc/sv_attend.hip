@@ -236,8 +236,6 @@ __device__ inline void mix_slowly(const uint16_t* values, const u32x4 (&w)[NT], 
   }
 }
 
-template <int N>
-struct Count { static constexpr int value = N; };
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
 
@@ -578,7 +576,7 @@ struct Join {
 };
 template <typename E, int D>
 __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a) {
-  constexpr int kLanes = Join<D>::kLanes;
+  constexpr int kLanes = Join<D>::kLanes, kStep = 4;
   const CacheView& c = a.c;
   const int b = blockIdx.x / a.R, r = blockIdx.x % a.R;
   const int heads = a.G * c.n_kv, hq = blockIdx.y * Join<D>::kHeads + threadIdx.x / kLanes;
@@ -609,8 +607,7 @@ __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a) {
       const int64_t at = ((int64_t)head * n_sets + first + nth + p0) * rows + row;
       const float* part_ml = (line ? a.part_ml[1] : a.part_ml[0]) + at * 2;
       const float* part_o = (line ? a.part_o[1] : a.part_o[0]) + at * D + d;
-      const auto take = [&](auto step, int k0) {
-        constexpr int kStep = decltype(step)::value;
+      const auto take = [&](int k0) {
         f32x2 ml[kStep];
         f32x4 y[kStep][2];
 #pragma unroll
@@ -632,8 +629,7 @@ __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a) {
           if (k0 + k < n) l += ml[k][1] * w, o[0] += y[k][0] * w, o[1] += y[k][1] * w;
         }
       };
-      if (n <= 4) take(Count<4>{}, 0);
-      else for (int k0 = 0; k0 < n; k0 += 8) take(Count<8>{}, k0);
+      for (int k0 = 0; k0 < n; k0 += kStep) take(k0);
     }
   }
   const float norm = 1.0f / l;
@@ -651,7 +647,10 @@ void launch(const AttendArgs& a, hipStream_t st) {
     hipLaunchKernelGGL((k_attend<E, D, 1>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
   else if (a.rows[kNarrow] == 32)
     hipLaunchKernelGGL((k_attend<E, D, 2>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
-  else if constexpr (D <= 128)
+  else if (a.rows[kNarrow] == 48) {
+    if constexpr (D <= 128)
+      hipLaunchKernelGGL((k_attend<E, D, 3>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
+  } else if constexpr (D <= 128)
     hipLaunchKernelGGL((k_attend<E, D, 4>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
   const unsigned gy = (a.G * a.c.n_kv + Join<D>::kHeads - 1) / Join<D>::kHeads;
   hipLaunchKernelGGL((k_join<E, D>), dim3(a.B * a.R, gy), dim3(kThreads), 0, st, a);

@@ -70,7 +70,7 @@ struct AttendPlan {
 inline int narrow_rows(int64_t rows, int head_dim) {
   if (rows <= 16) return 16;
   if (rows <= 32 || head_dim > 128) return 32;
-  return 64;
+  return rows <= 48 ? 48 : 64;
 }
 constexpr int wide_tiles(int head_dim) {  // tiles of 16 rows, of each of its four waves
   return head_dim > 128 ? 1 : head_dim > 64 ? 2 : 3;

@@ -195,8 +195,9 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
         }
         if (begins && cut[k][i].n > 0) {
           const int64_t nb = (key[k][i] - from + kBlock - 1) / kBlock;
-          sets[cut[k][i].line] += cut[k][i].n;
-          blocks[cut[k][i].line] += cut[k][i].n * nb;
+          const bool wide = cut[k][i].line == kWide;  // no array is indexed: it would leave the registers
+          sets[0] += wide ? 0 : cut[k][i].n, sets[1] += wide ? cut[k][i].n : 0;
+          blocks[0] += wide ? 0 : cut[k][i].n * nb, blocks[1] += wide ? cut[k][i].n * nb : 0;
         }
         from = key[k][i];
       }
@@ -235,15 +236,15 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
           int at = cc.line ? s[1] : s[0];
           int64_t y = cc.line ? x[1] : x[0];
           if (n[i] > 0 || k < 2) ss.first[k] = 2 * at + cc.line;
+          AttendSet* sets = cc.line ? a.p.sets[1] : a.p.sets[0];
           for (int q = 0; q < cc.n; ++q, ++at, y += nb)
-            a.p.sets[cc.line][at] = AttendSet{t_at[b], q * cc.per, min(cc.per, rows - q * cc.per), from,
-                                              key[k][i], list, k < 3 ? kFar : len[i], k == 3 && from == 0,
-                                              y, cc.per, 0};
+            sets[at] = AttendSet{t_at[b], q * cc.per, min(cc.per, rows - q * cc.per), from,
+                                 key[k][i], list, k < 3 ? kFar : len[i], k == 3 && from == 0, y, cc.per, 0};
           if (cc.line) s[1] = at, x[1] = y;
           else s[0] = at, x[0] = y;
         } else {
           // behind the sets that session f has in this line for a run of the level above
-          int at = set_at[cc.line][f];
+          int at = cc.line ? set_at[1][f] : set_at[0][f];
           if (k == 1 && first[0][run[0][i]] == f && cut[0][i].n > 0 && cut[0][i].line == cc.line)
             at += cut[0][i].n;
           ss.first[k] = 2 * at + cc.line;
