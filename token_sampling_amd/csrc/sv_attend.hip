@@ -643,15 +643,19 @@ void launch(const AttendArgs& a, hipStream_t st) {
   // rows that neighbours share go together, which may make them many
   if (a.B > 1 || a.R * a.G > a.rows[kNarrow])
     hipLaunchKernelGGL((k_attend_wide<E, D, wide_tiles(D)>), dim3(kPieces[kWide]), dim3(kThreads), 0, st, a);
-  if (a.rows[kNarrow] == 16)
-    hipLaunchKernelGGL((k_attend<E, D, 1>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
-  else if (a.rows[kNarrow] == 32)
-    hipLaunchKernelGGL((k_attend<E, D, 2>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
-  else if (a.rows[kNarrow] == 48) {
-    if constexpr (D <= 128)
-      hipLaunchKernelGGL((k_attend<E, D, 3>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
-  } else if constexpr (D <= 128)
-    hipLaunchKernelGGL((k_attend<E, D, 4>), dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
+  const auto narrow = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);
+  };
+  if constexpr (D > 128) {
+    narrow(k_attend<E, D, 1>);
+  } else {
+    switch (a.rows[kNarrow]) {
+      case 16: narrow(k_attend<E, D, 1>); break;
+      case 32: narrow(k_attend<E, D, 2>); break;
+      case 48: narrow(k_attend<E, D, 3>); break;
+      default: narrow(k_attend<E, D, 4>);
+    }
+  }
   const unsigned gy = (a.G * a.c.n_kv + Join<D>::kHeads - 1) / Join<D>::kHeads;
   hipLaunchKernelGGL((k_join<E, D>), dim3(a.B * a.R, gy), dim3(kThreads), 0, st, a);
 }

@@ -66,11 +66,17 @@ struct AttendPlan {
   AttendSet* sets[2];
 };
 
-// Rows of a narrow set at most, by what a round brings; and of a wide one.
+// Rows of a narrow set at most, by the rows that a round brings a key head, and of a
+// wide one.  Up to 64 rows a session's keys go into one narrow set, all of whose rows
+// have to fit a wave's registers: 64 sessions of 8192 tokens, 8 heads of 128, 64 rows,
+// take 465 us so and 497 as wide sets (heads of 64: 251 and 349), 68 rows 457 as wide
+// sets.  What is left of a wide set's session, the keys that not all rows see, goes in
+// sets of 48.  Heads of 256 leave room for 16 rows only (32 in registers: 399 against
+// 391 us for 16 rows, 449 against 446 for 32).
 inline int narrow_rows(int64_t rows, int head_dim) {
-  if (rows <= 16) return 16;
-  if (rows <= 32 || head_dim > 128) return 32;
-  return rows <= 48 ? 48 : 64;
+  if (rows <= 16 || head_dim > 128) return 16;
+  if (rows <= 32) return 32;
+  return rows > 48 && rows <= 64 ? 64 : 48;
 }
 constexpr int wide_tiles(int head_dim) {  // tiles of 16 rows, of each of its four waves
   return head_dim > 128 ? 1 : head_dim > 64 ? 2 : 3;
