@@ -677,10 +677,11 @@ int sv_cache_write(const sv_cache *cache, int32_t layer, const sv_rows *from, co
 /*
  * The plan of a round's attention: which keys and rows go together.  Where
  * neighbouring sessions (places without one between them do not count) have
- * the same leading pages, these are read once for all of them, on up to two
- * levels: what a run of sessions shares, and what parts of the run share
- * beyond it; so sessions that share should be listed side by side.  The result
- * depends on it by the order of its sums alone.  rows [B] int32 (NULL: R): the
+ * the same leading pages, and enough of them for it to be faster (some thousand
+ * tokens for few sessions, some hundred for many), these are read once for all
+ * of them, on up to two levels: what a run of sessions shares, and what parts of the
+ * run share beyond it; so sessions that share should be listed side by side.  The
+ * result depends on it by the order of its sums alone.  rows [B] int32 (NULL: R): the
  * session's rows of the round.  n_heads: query heads, a multiple of n_kv.
  * plan: DEVICE, sv_cache_plan_bytes(); it holds for every layer as long as lists,
  * lengths, slots and rows stay as they are.  status: SV_S_BAD_CACHE also where the

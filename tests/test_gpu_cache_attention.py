@@ -317,3 +317,51 @@ def test_many_sessions_share():
     slots = np.arange(n)
     slots[rng.random(n) < 0.1] = -1
     check(cache, ref, slots, rows, queries(rng, (n, 3, 2, 64), torch.bfloat16))
+
+
+@pytest.mark.parametrize("dim,dtype,Hq,R", [(128, torch.bfloat16, 16, 2), (256, torch.float16, 8, 3), (96, torch.bfloat16, 8, 65)])
+def test_long_shared(dim, dtype, Hq, R):
+    """Many sessions behind a prompt long enough to be read once for all, most of them
+    without rows this round; the first row block of the prompt's sets is partly filled, and
+    with 65 rows a session it takes several."""
+    rng = np.random.default_rng(dim)
+    n, common, page, Hkv = 150, 2304, 64, 8
+    cache = sv.make_cache(n + 1, 40 + 4 * n, 50, Hkv, dim, page=page, dtype=dtype)
+    sv.cache_reserve(cache, dev([common + 17]), slots=dev([n]))
+    sv.cache_keep(cache, dev([common + 17]), slots=dev([n]))
+    sv.cache_fork(cache, dev([n] * n), dev(range(n)))
+    rows = np.where(rng.random(n) < 0.06, rng.integers(1, R + 1, n), 0)
+    rows[[3, 77]] = R
+    assert not sv.cache_reserve(cache, dev(rows), slots=dev(range(n))).any()
+    for x in cache[:2]:
+        x.normal_()
+    from tests.cache_ref import Ref
+    slots = np.arange(n)
+    slots[10:13] = -1
+    check(cache, Ref(cache), slots, rows, queries(rng, (n, R, Hq, dim), dtype))
+
+
+def test_two_levels():
+    """Families within a batch: what all share and what a family shares beyond it, each long
+    enough to be read once."""
+    rng = np.random.default_rng(14)
+    fams, members, page, Hkv, dim, R = 3, 24, 256, 8, 256, 3
+    n = fams * members
+    cache = sv.make_cache(n + 1, 60 + 25 * fams + 2 * n, 40, Hkv, dim, page=page)
+    grow = lambda slots, add: (sv.cache_reserve(cache, dev(add), slots=dev(slots)),  # noqa: E731
+                               sv.cache_keep(cache, dev(add), slots=dev(slots)))
+    grow([n], [2048])
+    for f in range(fams):
+        head = f * members
+        sv.cache_fork(cache, dev([n]), dev([head]))
+        grow([head], [4700 if f else 100])  # the first family is too short for a level of its own
+        sv.cache_fork(cache, dev([head] * (members - 1)), dev(range(head + 1, head + members)))
+    rows = np.where(rng.random(n) < 0.1, rng.integers(1, R + 1, n), 0)
+    rows[[0, 30, 31, 60]] = R
+    assert not sv.cache_reserve(cache, dev(rows), slots=dev(range(n))).any()
+    for x in cache[:2]:
+        x.normal_()
+    from tests.cache_ref import Ref
+    ref = Ref(cache)
+    ref.sound()
+    check(cache, ref, np.arange(n), rows, queries(rng, (n, R, 16, dim), torch.bfloat16))

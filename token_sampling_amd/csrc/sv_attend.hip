@@ -70,8 +70,7 @@ __device__ inline Row row_at(const AttendArgs& a, const AttendSet& set, int head
              ((int64_t)row * (a.G * a.c.n_kv) + hq) * a.c.head_dim, set.base + r + 1};
 }
 
-// An accumulated value tile of a narrow or wide set goes out: as a partial result, or as
-// the result where it is whole.
+// Four dimensions of a whole result.
 template <typename E>
 __device__ inline void put4(char* out, f32x4 x, float norm) {
   uint2 y;
@@ -222,7 +221,9 @@ __device__ inline void mix_slowly(const uint16_t* values, const u32x4 (&w)[NT], 
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const uint32_t two = k & 4 ? (k & 2 ? w[t][3] : w[t][2]) : (k & 2 ? w[t][1] : w[t][0]);
-      p[t] = E::value((uint32_t)__shfl((int)two, k / 8 * 16 + col) >> (16 * (k & 1)) & 0xFFFFu);
+      uint32_t there = (uint32_t)__shfl((int)two, k / 8 * 16 + col);
+      pin(there);
+      p[t] = E::value(there >> (16 * (k & 1)) & 0xFFFFu);
     }
     const uint16_t* at = values + (k / 8 * 16 + g * 4) * 8 + k % 8;
 #pragma unroll
@@ -337,6 +338,7 @@ __device__ inline void narrow_set(const AttendArgs& a, const AttendSet& set, con
   for (int t = 0; t < NT; ++t) {
     l[t] += lane_xor<16>(l[t]);
     l[t] += lane_xor<32>(l[t]);
+    pin(l[t]);
     if (lane < 16) {
       red.m[wave][t * 16 + lane] = m[t];
       red.l[wave][t * 16 + lane] = l[t];
@@ -377,7 +379,12 @@ __device__ inline void narrow_set(const AttendArgs& a, const AttendSet& set, con
   }
 }
 
-// A workgroup goes over a piece of the narrow line, set by set.
+// A workgroup goes over a piece of the narrow line, set by set.  256 sessions of up to
+// 4096 tokens, 9 rows, 8 heads of 128 (36 rows a set): 2.5 GB in 455 us, 5.6 TB/s;
+// two sessions of 131072 tokens 195 us, 5.5 TB/s.  What bounds it there are the loads
+// in flight: a wave a SIMD with 16 to 32 KiB under way (48 rows take more than half of
+// the registers).  Sets of a few blocks are bound by their chains of loads: 239
+// sessions of 300 keys 113 us.
 template <typename E, int D, int NT>
 __global__ __launch_bounds__(kThreads) void k_attend(AttendArgs a) {
   __shared__ Meet<D, NT> red;
@@ -449,9 +456,14 @@ __device__ inline void in_turn(const u32x4 (*keys)[kWave], const u32x4 (*values)
 }
 
 // A workgroup goes over a piece of the wide line: its waves share the set's tiles of
-// 16 rows, NT each, and a tile of keys and values stands in LDS, brought there past the
-// registers while the one before it is in use.  Two workgroups a CU, so that one's
-// products run under the other's exponentials: that bounds NT, by 256 registers.
+// 16 rows, NT each, and tiles of 32 keys and values stand in a ring in LDS, brought
+// there past the registers two tiles ahead.  Two workgroups a CU, so that one's products
+// run under the other's exponentials: that bounds NT, by 256 registers.  4780 rows a
+// head over 8192 shared keys, 8 heads of 128: 1.6e11 operations in 200 us, 0.8 PFLOP/s,
+// where a large library product reaches 1.2.  The matrix unit is busy in 37% of the
+// cycles and the vector unit in 42%; without the loads it would take 173 us.  Tried and
+// left: NT = 3 (230 us, and 520 with registers spilled: a spilled value's load waits
+// for the tiles on their way), one workgroup a CU with NT = 4 (227 us).
 __device__ inline void to_lds(const char* from, void* to) {  // 16 bytes a lane, side by side
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)from,
                                    (__attribute__((address_space(3))) void*)to, 16, 0, 0);
@@ -549,6 +561,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void k_attend_wide(Atten
     for (int t = 0; t < NT; ++t) {
       l[t] += lane_xor<16>(l[t]);
       l[t] += lane_xor<32>(l[t]);
+      pin(l[t]);
       const int j = (t * kWaves + wave) * 16 + col;
       if (j >= set.n) continue;
 #pragma unroll
@@ -567,8 +580,10 @@ __device__ inline int piece_of(int64_t x, int64_t total, int64_t piece) {
 }
 
 // Joins the partial results of every row.  A lane has 8 dimensions of a row and head, a
-// wave some heads of a row, side by side; parts are loaded several at a time, as what
-// they wait for is memory.  NaN where the session failed.
+// wave some heads of a row, side by side; parts are loaded four at a time, as what they
+// wait for is memory (eight: 12 against 14 us for 640 rows of 32 parts, but 23 against
+// 19 for 38000 rows of two or three, whose waves then have too many registers).  NaN
+// where the session failed.
 template <int D>
 struct Join {
   static constexpr int kLanes = D == 96 ? 16 : D / 8;         // of a row and head

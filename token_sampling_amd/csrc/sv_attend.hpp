@@ -24,7 +24,7 @@ namespace sv {
 
 constexpr int kBlock = 128;     // keys
 constexpr int kNarrow = 0, kWide = 1;
-constexpr int kPieces[2] = {512, 512};  // of a line: two workgroups a CU, and one
+constexpr int kPieces[2] = {512, 512};  // of a line: two workgroups a CU
 constexpr int kFar = 1 << 30;   // no limit on keys
 
 struct AttendSet {
@@ -78,7 +78,7 @@ inline int narrow_rows(int64_t rows, int head_dim) {
   if (rows <= 32) return 32;
   return rows > 48 && rows <= 64 ? 64 : 48;
 }
-constexpr int wide_tiles(int head_dim) {  // tiles of 16 rows, of each of its four waves
+constexpr int wide_tiles(int head_dim) {  // tiles of 16 rows of each of four waves, in 256 registers
   return head_dim > 128 ? 1 : head_dim > 64 ? 2 : 3;
 }
 inline int wide_rows(int head_dim) { return 64 * wide_tiles(head_dim); }

@@ -61,6 +61,13 @@ __device__ inline int value_at(int u, int d, int head_dim) {
   return (u / 32 * (head_dim / 16) + d / 16) * 512 + (t / 8 * 16 + d % 16) * 8 + t % 8;
 }
 
+// Keeps x's computation where it stands, in every lane: what comes from other lanes must
+// not be fetched under a branch that only some lanes take.
+template <typename T>
+__device__ inline void pin(T& x) {
+  asm volatile("" : "+v"(x));
+}
+
 // Inclusive prefix sum over a workgroup of NT threads, and its total.
 template <int NT, typename T>
 __device__ inline T block_incl_scan(T v, T* smem, T& total) {

@@ -16,7 +16,6 @@ struct PlanArgs {
   int32_t G, B, R;       // query heads a key head
   int32_t narrow, wide;  // rows of a set
   int32_t pieces[2];
-  int32_t least;         // keys shared that are worth a set of their own
 };
 
 __device__ inline int place_of(const PlanArgs& a, int b) { return a.slots ? a.slots[b] : b; }
@@ -51,7 +50,6 @@ __global__ __launch_bounds__(kShared) void k_shared(PlanArgs a) {
       __syncthreads();
       const int whole = max(kBlock, c.page());
       keys = (int)(((int64_t)first << c.shift) / whole * whole);
-      if (keys < a.least) keys = 0;
     }
   }
   if (threadIdx.x == 0) a.p.shared[b] = keys;
@@ -68,13 +66,24 @@ __device__ inline Cut cut_rows(const PlanArgs& a, int64_t rows) {
   return Cut{kWide, n, (int)((rows + n - 1) / n + 15) / 16 * 16};
 }
 
+// Keys that n neighbours share are worth sets of their own from so many on.  Read by each
+// session they come from caches mostly, and a row's further part and the wide sets'
+// start cost some 20 us.  Measured at 8 heads of 128, a row and 9 rows a session: 4 sessions
+// break even at 6000 and 11000 keys, 16 at 13000 and 11000, 64 at 3000, 256 at 1500 and 1300
+// (of 8192 keys, 9 rows: 54 shared and 52 us unshared, 75 and 70, 149 and 197, 529
+// and 739).  Smaller heads bring fewer bytes.
+__device__ inline int worth(const PlanArgs& a, int n) {
+  return 180000000 / (a.c.n_kv * a.c.head_dim * min(max(n, 20), 140));
+}
+
 // The keys of a session's own, behind the `from` that it shares: where those end that
 // go into wide sets (whole blocks that all rows see, where the rows are many).
 __device__ inline int clear_end(const PlanArgs& a, int rows, int len, int from) {
   return (int64_t)rows * a.G > a.narrow ? max(from, len / kBlock * kBlock) : from;
 }
 
-// One workgroup, kPer sessions a thread.
+// One workgroup, kPer sessions a thread.  12 us for one session, 25 for 1024: chains of
+// dependent loads and a dozen barriers, once a round for all layers.
 template <int kPer>
 __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
   // by session: the first row's place; in each line the first set, and the blocks
@@ -152,7 +161,7 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
       int least = 1;
       if (level == 1 && b < a.B) {
         const int d = depth[0][run[0][i]];
-        least = (d == kNone ? 0 : d) + a.least;
+        least = (d == kNone ? 0 : d) + kBlock;
       }
       const bool starts = b < a.B && (b == 0 || shared[i] < least || (level == 1 && first[0][run[0][i]] == b));
       int64_t total;
@@ -182,7 +191,9 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
       for (int k = 0; k < kKinds; ++k) {
         bool begins = true;
         if (k < 2) {
-          const int r = run[k][i], d = depth[k][r] == kNone ? from : depth[k][r];
+          const int r = run[k][i];
+          int d = depth[k][r];
+          if (d == kNone || d - from < worth(a, first[k][r + 1] - first[k][r])) d = from;
           key[k][i] = d;
           if (d > from) cut[k][i] = cut_rows(a, (int64_t)(t_at[first[k][r + 1]] - t_at[first[k][r]]) * a.G);
           begins = first[k][r] == b;
@@ -325,7 +336,7 @@ extern "C" int sv_cache_plan(const sv_cache* cache, const int32_t* slots, const 
   (void)hipGetLastError();
   const PlanArgs a = {view_of(cache), plan_of(z, plan), slots, rows, status, G, B, R,
                       narrow_rows((int64_t)R * G, cache->head_dim), wide_rows(cache->head_dim),
-                      {kPieces[0], kPieces[1]}, 256};
+                      {kPieces[0], kPieces[1]}};
   hipLaunchKernelGGL(k_shared, dim3(B), dim3(kShared), 0, st, a);
   if (B <= kOne) hipLaunchKernelGGL(k_plan<1>, dim3(1), dim3(kOne), 0, st, a);
   else hipLaunchKernelGGL(k_plan<SV_CACHE_B_MAX / kOne>, dim3(1), dim3(kOne), 0, st, a);
