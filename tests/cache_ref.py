@@ -170,8 +170,8 @@ class Ref:
         """Outputs [B, R, Hq, D] in 64 bits (NaN where not defined) and their bounds.
 
         The bound, with u the relative rounding of dtype: u |o| for the output, u A for
-        the weights (A = sum_t w_t |v_t|; fp16 weights, at most 1 and next to a sum of
-        at least 1, are off by 2^-25 where they are subnormal), and in binary32
+        the weights (A = sum_t w_t |v_t|; fp16 weights, whose sum is at least 1
+        before it is divided out, are off by 2^-25 where they are subnormal), and in binary32
         (n + 4) 2^-23 A for sums of n terms that join in any order, and for the scores,
         D products summed, scaled twice and put into exp2, 2 A max_t e_t with e_t =
         (D + 8) 2^-23 scale sum_d |q_d k_td|."""

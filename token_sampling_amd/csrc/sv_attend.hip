@@ -655,8 +655,7 @@ __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a) {
 
 template <typename E, int D>
 void launch(const AttendArgs& a, hipStream_t st) {
-  // rows that neighbours share go together, which may make them many
-  if (a.B > 1 || a.R * a.G > a.rows[kNarrow])
+  if (may_be_wide((int64_t)a.R * a.G, a.c.n_kv, D, a.B, (int64_t)a.c.max_pages << a.c.shift))
     hipLaunchKernelGGL((k_attend_wide<E, D, wide_tiles(D)>), dim3(kPieces[kWide]), dim3(kThreads), 0, st, a);
   const auto narrow = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(kPieces[kNarrow]), dim3(kThreads), 0, st, a);

@@ -83,6 +83,21 @@ constexpr int wide_tiles(int head_dim) {  // tiles of 16 rows of each of four wa
 }
 inline int wide_rows(int head_dim) { return 64 * wide_tiles(head_dim); }
 
+// Keys that n neighbours share are worth sets of their own from so many on.  Read by each
+// session they come from caches mostly, and a row's further part and the wide sets'
+// start cost some 20 us.  Measured at 8 heads of 128, a row and 9 rows a session: 4 sessions
+// break even at 6000 and 11000 keys, 16 at 13000 and 11000, 64 at 3000, 256 at 1500 and 1300
+// (of 8192 keys, 9 rows: 54 shared and 52 us unshared, 75 and 70, 149 and 197, 529
+// and 739).  Smaller heads bring fewer bytes.
+__host__ __device__ inline int worth(int n_kv, int head_dim, int n) {
+  return 180000000 / (n_kv * head_dim * (n < 20 ? 20 : n > 140 ? 140 : n));
+}
+// Whether a plan can hold wide sets: rows too many for a narrow one, or B sessions of
+// `most` tokens that can share enough.  Where it cannot, their kernel is not launched.
+inline bool may_be_wide(int64_t rows, int n_kv, int head_dim, int B, int64_t most) {
+  return rows > narrow_rows(rows, head_dim) || (B > 1 && most >= worth(n_kv, head_dim, B));
+}
+
 struct PlanSizes {
   int64_t sets[2], bytes, sess, starts, shared, row_of, set_at[2];
 };

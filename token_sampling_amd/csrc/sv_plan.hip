@@ -66,16 +66,6 @@ __device__ inline Cut cut_rows(const PlanArgs& a, int64_t rows) {
   return Cut{kWide, n, (int)((rows + n - 1) / n + 15) / 16 * 16};
 }
 
-// Keys that n neighbours share are worth sets of their own from so many on.  Read by each
-// session they come from caches mostly, and a row's further part and the wide sets'
-// start cost some 20 us.  Measured at 8 heads of 128, a row and 9 rows a session: 4 sessions
-// break even at 6000 and 11000 keys, 16 at 13000 and 11000, 64 at 3000, 256 at 1500 and 1300
-// (of 8192 keys, 9 rows: 54 shared and 52 us unshared, 75 and 70, 149 and 197, 529
-// and 739).  Smaller heads bring fewer bytes.
-__device__ inline int worth(const PlanArgs& a, int n) {
-  return 180000000 / (a.c.n_kv * a.c.head_dim * min(max(n, 20), 140));
-}
-
 // The keys of a session's own, behind the `from` that it shares: where those end that
 // go into wide sets (whole blocks that all rows see, where the rows are many).
 __device__ inline int clear_end(const PlanArgs& a, int rows, int len, int from) {
@@ -193,7 +183,7 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
         if (k < 2) {
           const int r = run[k][i];
           int d = depth[k][r];
-          if (d == kNone || d - from < worth(a, first[k][r + 1] - first[k][r])) d = from;
+          if (d == kNone || d - from < worth(c.n_kv, c.head_dim, first[k][r + 1] - first[k][r])) d = from;
           key[k][i] = d;
           if (d > from) cut[k][i] = cut_rows(a, (int64_t)(t_at[first[k][r + 1]] - t_at[first[k][r]]) * a.G);
           begins = first[k][r] == b;
