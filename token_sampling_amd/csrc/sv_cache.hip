@@ -416,12 +416,13 @@ __global__ __launch_bounds__(kWrite) void k_write(WriteArgs a) {
       octet = (int)(item % a.octets);
       n = a.rows ? min(max(a.rows[b], 0), a.R) : a.R;
     }
-    const int h = n > 0 ? (a.slots ? a.slots[b] : b) : -1;
+    // items before the first session's (offsets[0] rows belong to none) have octet < 0
+    const int h = n > 0 && octet >= 0 ? (a.slots ? a.slots[b] : b) : -1;
     const bool some = h >= 0 && h < c.n_slots;
     const int64_t len = some ? c.lens[h] : 0;
     const int64_t pos = (len / 8 + octet) * 8;  // the octet's first position
-    const int e0 = pos < len ? (int)(len - pos) : 0;
-    int e1 = some && len >= 0 ? (int)min((int64_t)8, len + n - pos) : 0;
+    const int e0 = some && pos < len ? (int)(len - pos) : 0;
+    const int e1 = some && len >= 0 ? (int)min((int64_t)8, len + n - pos) : 0;
     // the rows, which do not wait for the page
     const int64_t row0 = lo + pos - len;  // row of element 0 of the octet (may lie before the rows)
     const char* kp = a.k + 2 * (b * a.k_session + row0 * a.k_row + head * a.k_head + d);
@@ -438,11 +439,10 @@ __global__ __launch_bounds__(kWrite) void k_write(WriteArgs a) {
       page = c.table[(int64_t)h * c.max_pages + (pos >> c.shift)];
       if (page < 0 || page >= c.n_pages || c.refs[page] != 1) page = -1;
     }
-    if (page < 0) e1 = 0;
     const int u = (int)(pos & (c.page() - 1));
     const int64_t at = a.base + max(page, 0) * c.page_elems() + head * c.head_elems();
     const int64_t k_at = 2 * (at + key_at(u, d, c.head_dim)), v_at = 2 * (at + value_at(u, d, c.head_dim));
-    const int span = e0 | max(e1, 0) << 4;
+    const int span = page < 0 ? 0 : e0 | e1 << 4;  // 0: stores nothing
     // keys: four tokens of 16 threads at a time; of a thread's pieces the one of token e
     // stands at place e ^ lane % 8, so that neither side meets in one bank
 #pragma unroll
