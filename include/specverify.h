@@ -699,7 +699,8 @@ int sv_cache_plan(const sv_cache *cache, const int32_t *slots, const int32_t *ro
  * t = 0 .. lens + r, keys and values of head h / (n_heads / n_kv).  The rows' own
  * keys and values must be written.  Scores, weights' sums and outputs are kept
  * in binary32; a weight is rounded to dtype before it meets the values, as the
- * matrix instructions take it, and the output once.  What a row does not see has no part in it, NaN and infinities
+ * matrix instructions take it (half's small weights to 2^-32 of the row's largest),
+ * and the output once.  What a row does not see has no part in it, NaN and infinities
  * included.  q [B, R, n_heads, head_dim] of dtype at element strides q_session,
  * q_row, q_head (>= 0, multiples of 8; 16-byte aligned); out the same shape,
  * contiguous, not overlapping q.  Rows that a session does not use are neither read nor

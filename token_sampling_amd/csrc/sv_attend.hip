@@ -18,6 +18,7 @@ struct Bf {
   typedef __bf16 vec8 __attribute__((ext_vector_type(8)));
   typedef __bf16 vec2 __attribute__((ext_vector_type(2)));
   static constexpr uint32_t kExp = 0x7F80u;  // exponent of infinities and NaN
+  static constexpr float kLift = 0.0f;       // see kSlack
   __device__ static inline float value(uint32_t bits) { return __uint_as_float(bits << 16); }
   __device__ static inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(vec8, a),
@@ -28,6 +29,7 @@ struct Hf {
   typedef _Float16 vec8 __attribute__((ext_vector_type(8)));
   typedef _Float16 vec2 __attribute__((ext_vector_type(2)));
   static constexpr uint32_t kExp = 0x7C00u;
+  static constexpr float kLift = 7.0f;
   __device__ static inline float value(uint32_t bits) { return (float)__builtin_bit_cast(_Float16, (uint16_t)bits); }
   __device__ static inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(vec8, a),
@@ -112,14 +114,20 @@ __device__ inline void score(const u32x4 (&kf)[kC], const u32x4 (&q)[kC], f32x4&
 }
 
 // Scores become weights: 2^(z * scale - m), with m a value near the row's largest
-// score so far.  m follows the largest only where a score exceeds it by kSlack,
-// which after the first tiles hardly happens: the lanes need not agree on a tile's
-// largest, and what is summed is seldom multiplied.  Weights reach 2^kSlack, which
-// costs no digits in binary32 or in either 16-bit type.
+// score so far.  m follows the largest only where a score's weight exceeds what that one
+// had by 2^kSlack, which after the first tiles hardly happens: the lanes need not agree on
+// a tile's largest, and what is summed is seldom multiplied.  The largest score's weight
+// lies between 2^kLift and 2^(kLift + kSlack).  That costs no digits in binary32 or
+// bfloat16, whose exponents reach far enough with a kLift of 0.  Halves end at 2^16 and
+// have fewer digits below 2^-14, so kLift is 7 there: a key's weight is off by half its last
+// digit or 2^-32 of the largest, and 131072 keys together by 2^-15 at most (without the
+// lift 2^-25 and 2^-8: they would be lost from the values but not from the sum).
 constexpr float kSlack = 8.0f;
+template <typename E>
+constexpr float kReach = E::kLift + kSlack;
 constexpr float kLowest = -3.402823466e38f;  // m of a row that has seen nothing
 // Hidden scores are -inf; true where a row's m has to follow.
-template <bool kEdge, int NT>
+template <typename E, bool kEdge, int NT>
 __device__ inline bool look_up(f32x4 (&z)[NT][2], float (&top)[NT], float scale, int key, const int (&lim)[NT],
                                const float (&m)[NT]) {
   bool far = false;
@@ -134,16 +142,16 @@ __device__ inline bool look_up(f32x4 (&z)[NT][2], float (&top)[NT], float scale,
 #pragma unroll
     for (int e = 1; e < 8; ++e) top[t] = fmaxf(top[t], z[t][e / 4][e % 4]);
     top[t] *= scale;
-    far |= top[t] > m[t] + kSlack;
+    far |= top[t] > m[t] + kReach<E>;
   }
   return __any(far);
 }
-template <int NT, int kN>
+template <typename E, int NT, int kN>
 __device__ inline void follow(const float (&top)[NT], float (&m)[NT], float (&l)[NT], f32x4 (&o)[NT][kN]) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float now = fmaxf(top[t], lane_xor<16>(top[t]));
-    now = fmaxf(m[t], fmaxf(now, lane_xor<32>(now)));
+    now = fmaxf(m[t], fmaxf(now, lane_xor<32>(now)) - E::kLift);
     const float keep = __builtin_amdgcn_exp2f(m[t] - now);
     m[t] = now;
     l[t] *= keep;
@@ -172,7 +180,7 @@ template <typename E, bool kEdge, int NT, int kN>
 __device__ inline void weigh(f32x4 (&z)[NT][2], u32x4 (&w)[NT], float scale, int key, const int (&lim)[NT],
                              float (&m)[NT], float (&l)[NT], f32x4 (&o)[NT][kN]) {
   float top[NT], sum[NT];
-  if (look_up<kEdge>(z, top, scale, key, lim, m)) follow(top, m, l, o);
+  if (look_up<E, kEdge>(z, top, scale, key, lim, m)) follow<E>(top, m, l, o);
   powers<E>(z, w, sum, scale, m);
 #pragma unroll
   for (int t = 0; t < NT; ++t) l[t] += sum[t];
@@ -531,11 +539,11 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void k_attend_wide(Atten
 #pragma unroll
       for (int t = 0; t < NT; ++t) score<E>(kf, q[t], z[t][h]);
     }
-    look_up<false>(z, top, a.scale, 0, no_limit, m);
+    look_up<E, false>(z, top, a.scale, 0, no_limit, m);
     bool far = true;
     for (int i = 0;;) {
       if (far) {
-        follow(top, m, l, o);
+        follow<E>(top, m, l, o);
         powers<E>(z, w, sum, a.scale, m);
       }
       if (i + 1 == tiles) break;
@@ -547,7 +555,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void k_attend_wide(Atten
         in_turn<E>(&tile[(i + 1) % kRing][0], &tile[i % kRing][2 * kC], q, w, o, z, top, sum, a.scale, m);
         far = false;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) far |= (top[t] *= a.scale) > m[t] + kSlack;
+        for (int t = 0; t < NT; ++t) far |= (top[t] *= a.scale) > m[t] + kReach<E>;
         far = __any(far);
         ++i;
       } while (!far && i + 1 < tiles);
