@@ -610,9 +610,9 @@ typedef struct sv_cache {
  * SV_S_*.  1 <= B <= SV_CACHE_B_MAX.  Return codes: SV_OK, SV_ERR_ARG,
  * SV_ERR_WORKSPACE or SV_ERR_DEVICE. */
 
-/* Bytes of device workspace for sv_cache_reserve, sv_cache_compact (contents
- * need not be initialised; calls that overlap need distinct ones).  0 if the
- * sizes are out of range. */
+/* Bytes of device workspace for sv_cache_reserve, sv_cache_compact (16-byte
+ * aligned; contents need not be initialised; calls that overlap need distinct
+ * ones).  0 if the sizes are out of range. */
 size_t sv_cache_workspace_bytes(const sv_cache *cache, int32_t B);
 
 /*

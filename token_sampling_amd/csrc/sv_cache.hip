@@ -511,6 +511,7 @@ extern "C" int sv_cache_reserve(const sv_cache* cache, const int32_t* slots, con
                                 size_t workspace_bytes, void* stream) {
   using namespace sv;
   if (!cache_ok(cache) || !add || !workspace || !sessions_ok(cache, slots, B)) return SV_ERR_ARG;
+  if ((uintptr_t)workspace % 16 != 0) return SV_ERR_ARG;
   if (workspace_bytes < scratch_bytes(cache, B)) return SV_ERR_WORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
@@ -547,7 +548,7 @@ extern "C" int sv_cache_fork(const sv_cache* cache, const int32_t* src, const in
 extern "C" int sv_cache_compact(const sv_cache* cache, int32_t* used, int32_t* moved,
                                 void* workspace, size_t workspace_bytes, void* stream) {
   using namespace sv;
-  if (!cache_ok(cache) || !used || !workspace) return SV_ERR_ARG;
+  if (!cache_ok(cache) || !used || !workspace || (uintptr_t)workspace % 16 != 0) return SV_ERR_ARG;
   if (workspace_bytes < scratch_bytes(cache, 1)) return SV_ERR_WORKSPACE;
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();
