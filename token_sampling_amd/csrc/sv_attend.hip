@@ -732,14 +732,15 @@ extern "C" int sv_cache_attention(const sv_cache* cache, int32_t layer, const vo
   if (((uintptr_t)q | (uintptr_t)plan | (uintptr_t)out | (uintptr_t)workspace) % 16 != 0)
     return SV_ERR_ARG;
   if (!stride_ok(q_session) || !stride_ok(q_row) || !stride_ok(q_head)) return SV_ERR_ARG;
-  if (!(scale > 0) || !(scale < INFINITY)) return SV_ERR_ARG;
+  const float in_twos = scale * 1.44269504088896340736f;  // of powers of two
+  if (!(in_twos > 0) || !(in_twos < INFINITY)) return SV_ERR_ARG;
   if (workspace_bytes < need) return SV_ERR_WORKSPACE;
   const int G = n_heads / cache->n_kv;
   const PlanSizes z = plan_sizes(B, R, G, cache->head_dim);
   const Parts parts = parts_of(cache, z, R, G);
   AttendArgs a = {view_of(cache), plan_of(z, (void*)plan), (const char*)q, q_session, q_row, q_head,
                   (char*)out, {}, {}, {parts.rows[0], parts.rows[1]},
-                  scale * 1.44269504088896340736f, 0, G, B, R};
+                  in_twos, 0, G, B, R};
   float* part = (float*)workspace;
   for (int line = 0; line < 2; ++line) {
     const int64_t rows = parts.slots[line] * parts.rows[line];
