@@ -703,7 +703,7 @@ int sv_cache_plan(const sv_cache *cache, const int32_t *slots, const int32_t *ro
  * and the output once.  What a row does not see has no part in it, NaN and infinities
  * included.  q [B, R, n_heads, head_dim] of dtype at element strides q_session,
  * q_row, q_head (>= 0, multiples of 8; 16-byte aligned); out the same shape,
- * contiguous, not overlapping q.  Rows that a session does not use are neither read nor
+ * contiguous, not overlapping q or the cache.  Rows that a session does not use are neither read nor
  * written; all R rows of a failed session become NaN.  scale > 0, and
  * finite times log2(e) in binary32.
  * plan: of sv_cache_plan with the same cache, n_heads, B and R.  workspace:

@@ -1323,9 +1323,13 @@ def cache_attention(cache, layer, q, plan, scale=None, out=None, workspace=None,
             out = torch.empty(shape, dtype=q.dtype, device=dev)
         else:
             _want(out, "out", q.dtype, shape, dev)
-            hi = p_q + 2 * (sum(s * (n - 1) for s, n in zip(strides, shape)) + c.head_dim)
-            if out.data_ptr() < hi and p_q < out.data_ptr() + 2 * out.numel():
+            lo = out.data_ptr()
+            hi = lo + 2 * out.numel()
+            if lo < p_q + 2 * (sum(s * (n - 1) for s, n in zip(strides, shape)) + c.head_dim) and p_q < hi:
                 raise ValueError("out overlaps q")
+            plane = 2 * cache.k.numel()
+            if (lo < c.k + plane and c.k < hi) or (lo < c.v + plane and c.v < hi):
+                raise ValueError("out overlaps the cache")
         workspace, size = _bytes(workspace, plan.workspace_bytes, "workspace", dev)
         rc = lib().sv_cache_attention(ctypes.byref(c), layer, p_q, *strides, scale, p_plan,
                                       n_heads, B, R, out.data_ptr(),
