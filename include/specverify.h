@@ -639,9 +639,11 @@ int sv_cache_keep(const sv_cache *cache, const int32_t *slots, const int32_t *co
 
 /*
  * Slot dst[i] takes over the tokens of slot src[i]: its list of pages as far as its
- * length reaches, without a copy.  dst must be empty (held = 0), be listed once
- * and not be a src of the call: SV_S_BAD_CACHE.  Several dst may have one src.  A
- * place with src or dst of -1 is left alone.
+ * length reaches, without a copy.  SV_S_BAD_CACHE: dst is not empty (held != 0) or
+ * listed twice, or src is also listed as a dst, which may be taking over tokens
+ * at once (of 0 -> 3 and 3 -> 5 the first is served, the second fails).  Several
+ * dst may have one src.  A place with src or dst of -1 is left alone, but the dst
+ * that it names counts as listed.
  */
 int sv_cache_fork(const sv_cache *cache, const int32_t *src, const int32_t *dst, int32_t n,
                   int32_t *status, void *stream);

@@ -1165,9 +1165,9 @@ def cache_keep(cache, count, slots=None, absolute=False, status=None, stream=Non
 
 
 def cache_fork(cache, src, dst, status=None, stream=None):
-    """sv_cache_fork: slot dst[i] (empty) takes over the tokens of slot src[i], [n]
-    int32 each (-1: none), sharing its pages.  Returns status [n] int32: 0 or
-    S_BAD_CACHE."""
+    """sv_cache_fork: slot dst[i] (empty, listed once) takes over the tokens of slot
+    src[i] (no dst of this call), [n] int32 each (-1: none), sharing its pages.
+    Returns status [n] int32: 0 or S_BAD_CACHE."""
     import torch
 
     dev = _device_of(src, "src")
