@@ -709,7 +709,12 @@ int sv_cache_plan(const sv_cache *cache, const int32_t *slots, const int32_t *ro
  * written; all R rows of a failed session become NaN.  scale > 0, and
  * finite times log2(e) in binary32.
  * plan: of sv_cache_plan with the same cache, n_heads, B and R.  workspace:
- * sv_cache_attention_bytes(); calls that overlap need distinct ones.
+ * sv_cache_attention_bytes(), 16-byte aligned; calls that overlap need distinct
+ * ones.  It holds B * R * n_heads partial results of 4 * (head_dim + 2) bytes: one
+ * each; one more where R * n_heads / n_kv > 64 (16 for a head_dim of 256); two more
+ * where B sessions of max_pages pages can share enough (sv_cache_plan); and up to
+ * 51 MB for what the split cuts.  256 sessions of 9 rows and 32 heads of 128 in a long
+ * cache take 162 MB, 1024 of 65 rows 4.5 GB: such a batch may be given in parts.
  */
 size_t sv_cache_attention_bytes(const sv_cache *cache, int32_t n_heads, int32_t B, int32_t R);
 int sv_cache_attention(const sv_cache *cache, int32_t layer, const void *q, int64_t q_session,

@@ -47,8 +47,9 @@ struct AttendArgs {
   const char* q;
   int64_t q_session, q_row, q_head;
   char* out;
-  float* part_o[2];   // of the lines' partial results: [slots][rows][head_dim]
-  float* part_ml[2];  // [slots][rows][2]
+  float* part_o;      // partial results: [places][head_dim]
+  float* part_ml;     // [places][2]
+  int64_t cuts[2];    // where the places by piece begin, of each line
   int32_t rows[2];    // of a set at most
   float scale;        // times log2 e
   int64_t base;       // the layer's first element
@@ -85,8 +86,17 @@ __device__ inline void put4(char* out, f32x4 x, float norm) {
 struct Cursor {
   int64_t x, end;
   int s, head, blk, sets, piece;
-  __device__ int64_t part() const { return (int64_t)head * sets + s + piece; }
 };
+// The first row's place among the partial results.
+__device__ inline int64_t by_row(const AttendArgs& a, const AttendSet& set, int head) {
+  return ((int64_t)set.kind * a.c.n_kv + head) * a.B * a.R * a.G + (int64_t)set.t0 * a.G + set.j0;
+}
+__device__ inline int64_t by_piece(const AttendArgs& a, int line, int piece) {
+  return a.cuts[line] + (int64_t)piece * a.rows[line];
+}
+__device__ inline int64_t place(const AttendArgs& a, int line, const AttendSet& set, const Cursor& at) {
+  return at.blk == 0 ? by_row(a, set, at.head) : by_piece(a, line, at.piece);
+}
 constexpr int kXcds = 8;
 __device__ inline bool begin(const AttendArgs& a, int line, Cursor& at) {
   const int64_t total = a.p.head->total[line], piece = a.p.head->piece[line];
@@ -353,7 +363,7 @@ __device__ inline void narrow_set(const AttendArgs& a, const AttendSet& set, con
     }
   }
   __syncthreads();
-  const int64_t part = at.part();
+  const int64_t part = place(a, kNarrow, set, at);
   const bool whole = set.alone && cnt == set.blocks();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -378,10 +388,10 @@ __device__ inline void narrow_set(const AttendArgs& a, const AttendSet& set, con
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) all += red.o[w][i][lane];
         if (whole) put4<E>(out + 2 * (i * 16 + g * 4), all, norm);
-        else *(f32x4*)(a.part_o[kNarrow] + (part * kMax * 16 + j) * D + i * 16 + g * 4) = all;
+        else *(f32x4*)(a.part_o + (part + j) * D + i * 16 + g * 4) = all;
       }
       if (!whole && wave == 0 && g == 0)
-        *(f32x2*)(a.part_ml[kNarrow] + (part * kMax * 16 + j) * 2) = f32x2{top, sum};
+        *(f32x2*)(a.part_ml + (part + j) * 2) = f32x2{top, sum};
     }
     __syncthreads();
   }
@@ -564,7 +574,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void k_attend_wide(Atten
     for (int t = 0; t < NT; ++t) l[t] += sum[t];
     const u32x4(*last)[kWave] = &tile[(tiles - 1) % kRing][2 * kC];
     mix<E>([&](int j) { return last[j][lane]; }, w, o);
-    const int64_t part = at.part();
+    const int64_t part = place(a, kWide, set, at);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       l[t] += lane_xor<16>(l[t]);
@@ -574,8 +584,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void k_attend_wide(Atten
       if (j >= set.n) continue;
 #pragma unroll
       for (int i = 0; i < kN; ++i)
-        *(f32x4*)(a.part_o[kWide] + (part * a.rows[kWide] + j) * D + i * 16 + g * 4) = o[t][i];
-      if (g == 0) *(f32x2*)(a.part_ml[kWide] + (part * a.rows[kWide] + j) * 2) = f32x2{m[t], l[t]};
+        *(f32x4*)(a.part_o + (part + j) * D + i * 16 + g * 4) = o[t][i];
+      if (g == 0) *(f32x2*)(a.part_ml + (part + j) * 2) = f32x2{m[t], l[t]};
     }
     advance(at, cnt);
   }
@@ -625,20 +635,20 @@ __global__ __launch_bounds__(kThreads) void k_join(AttendArgs a) {
       const int64_t x = head * blocks + set.cum + (int64_t)nth * nb;
       const int p0 = piece_of(x, total, piece), n = piece_of(x + nb - 1, total, piece) - p0 + 1;
       if (n == 1 && set.alone) return;
+      // the first part's place by row (set is the first over its keys, j the row from there),
+      // the others' by piece
       const int rows = line ? a.rows[1] : a.rows[0];
-      const int n_sets = line ? lines.sets[1] : lines.sets[0];
-      const int64_t at = ((int64_t)head * n_sets + first + nth + p0) * rows + row;
-      const float* part_ml = (line ? a.part_ml[1] : a.part_ml[0]) + at * 2;
-      const float* part_o = (line ? a.part_o[1] : a.part_o[0]) + at * D + d;
+      const int64_t at0 = by_row(a, set, head) + j, at1 = (line ? a.cuts[1] : a.cuts[0]) + (int64_t)p0 * rows + row;
       const auto take = [&](int k0) {
         f32x2 ml[kStep];
         f32x4 y[kStep][2];
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
-          const int64_t to = (int64_t)min(k0 + k, n - 1) * rows;
-          ml[k] = *(const f32x2*)(part_ml + to * 2);
-          y[k][0] = *(const f32x4*)(part_o + to * D);
-          y[k][1] = *(const f32x4*)(part_o + to * D + 4);
+          const int nth_part = min(k0 + k, n - 1);
+          const int64_t at = nth_part == 0 ? at0 : at1 + (int64_t)nth_part * rows;
+          ml[k] = *(const f32x2*)(a.part_ml + at * 2);
+          y[k][0] = *(const f32x4*)(a.part_o + at * D + d);
+          y[k][1] = *(const f32x4*)(a.part_o + at * D + d + 4);
         }
         float now = m;
 #pragma unroll
@@ -693,20 +703,21 @@ void launch_dim(const AttendArgs& a, hipStream_t st) {
 
 bool stride_ok(int64_t s) { return s >= 0 && s % 8 == 0 && s <= ((int64_t)1 << 40); }
 
-// Slots for partial results: one a set and head, and one for every cut.
+// Places for partial results: one a row and head for each kind of sets that can occur,
+// and a set's rows for each piece of a line.
 struct Parts {
-  int64_t slots[2], bytes;
-  int32_t rows[2];
+  int64_t by_row, places;
+  size_t bytes;
 };
-Parts parts_of(const sv_cache* c, const PlanSizes& z, int32_t R, int32_t G) {
+Parts parts_of(const sv_cache* c, int32_t B, int32_t R, int32_t G) {
+  const int64_t rows = (int64_t)R * G, most = (int64_t)c->max_pages * c->page;
+  const int narrow = narrow_rows(rows, c->head_dim);
+  const int kinds = 1 + (rows > narrow) + (may_share(c->n_kv, c->head_dim, B, most) ? 2 : 0);
   Parts p;
-  p.rows[kNarrow] = narrow_rows((int64_t)R * G, c->head_dim);
-  p.rows[kWide] = wide_rows(c->head_dim);
-  p.bytes = 0;
-  for (int line = 0; line < 2; ++line) {
-    p.slots[line] = z.sets[line] * c->n_kv + kPieces[line];
-    p.bytes += p.slots[line] * p.rows[line] * (c->head_dim + 2) * 4;
-  }
+  p.by_row = (int64_t)kinds * c->n_kv * B * rows;
+  p.places = p.by_row + (int64_t)kPieces[kNarrow] * narrow;
+  if (may_be_wide(rows, c->n_kv, c->head_dim, B, most)) p.places += (int64_t)kPieces[kWide] * wide_rows(c->head_dim);
+  p.bytes = (size_t)p.places * (c->head_dim + 2) * 4;
   return p;
 }
 
@@ -718,7 +729,7 @@ extern "C" size_t sv_cache_attention_bytes(const sv_cache* cache, int32_t n_head
   using namespace sv;
   if (sv_cache_plan_bytes(cache, n_heads, B, R) == 0) return 0;
   const int G = n_heads / cache->n_kv;
-  return (size_t)parts_of(cache, plan_sizes(B, R, G, cache->head_dim), R, G).bytes;
+  return parts_of(cache, B, R, G).bytes;
 }
 
 extern "C" int sv_cache_attention(const sv_cache* cache, int32_t layer, const void* q,
@@ -737,17 +748,13 @@ extern "C" int sv_cache_attention(const sv_cache* cache, int32_t layer, const vo
   if (workspace_bytes < need) return SV_ERR_WORKSPACE;
   const int G = n_heads / cache->n_kv;
   const PlanSizes z = plan_sizes(B, R, G, cache->head_dim);
-  const Parts parts = parts_of(cache, z, R, G);
-  AttendArgs a = {view_of(cache), plan_of(z, (void*)plan), (const char*)q, q_session, q_row, q_head,
-                  (char*)out, {}, {}, {parts.rows[0], parts.rows[1]},
-                  in_twos, 0, G, B, R};
+  const Parts parts = parts_of(cache, B, R, G);
+  const int32_t narrow = narrow_rows((int64_t)R * G, cache->head_dim);
   float* part = (float*)workspace;
-  for (int line = 0; line < 2; ++line) {
-    const int64_t rows = parts.slots[line] * parts.rows[line];
-    a.part_o[line] = part;
-    a.part_ml[line] = part + rows * cache->head_dim;
-    part += rows * (cache->head_dim + 2);
-  }
+  AttendArgs a = {view_of(cache), plan_of(z, (void*)plan), (const char*)q, q_session, q_row, q_head, (char*)out,
+                  part, part + parts.places * cache->head_dim,
+                  {parts.by_row, parts.by_row + (int64_t)kPieces[kNarrow] * narrow},
+                  {narrow, wide_rows(cache->head_dim)}, in_twos, 0, G, B, R};
   a.base = layer * a.c.layer_elems();
   hipStream_t st = (hipStream_t)stream;
   (void)hipGetLastError();

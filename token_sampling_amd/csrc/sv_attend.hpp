@@ -10,10 +10,12 @@
 // sees all of its keys, what rows see in part is left to narrow ones.  Keys are counted in
 // blocks of kBlock.  The narrow sets' blocks stand in one line, the first key head's,
 // then the second's and so on, the wide sets' in another; a line is cut into equal
-// pieces, a piece a workgroup.  Piece i leaves a partial result (largest score, sum,
-// weighted values) for every set and head that it touches, in slot head * sets + set
-// + i, and where a set and head lie in one piece and nothing else belongs to their
-// rows, the result itself.
+// pieces, a piece a workgroup.  A piece leaves a partial result (largest score, sum,
+// weighted values) for every set and head that it touches, and where a set and head lie
+// in one piece and nothing else belongs to their rows, the result itself.  A row is in at
+// most one set of a kind (below), so the partial result of a set's first blocks has its
+// place by kind, head and row; what a piece finds of a set that began in the one before,
+// one at most, has its place by the piece.
 // An XCD has neighbouring pieces (its workgroups are every eighth): sets of many rows
 // over the same keys go over a head's keys in one L2.
 #pragma once
@@ -37,14 +39,16 @@ struct AttendSet {
   int32_t alone; // nothing else belongs to these rows
   int64_t cum;   // blocks of the sets before
   int32_t per;   // rows of each but the last set over the same keys
-  int32_t pad;
+  int32_t kind;  // the place of its kind among the partial results
   __host__ __device__ int blocks() const { return (key1 - key0 + kBlock - 1) / kBlock; }
 };
 static_assert(sizeof(AttendSet) == 48, "AttendSet layout");
 
 // A session's rows stand in the sets from first[0] (its run's shared keys), first[1]
 // (its run's in that run), first[2] (its own keys that all its rows see, where these
-// are many) and first[3] (its other keys) on: 2 * set + line, -1: none.
+// are many) and first[3] (its other keys) on: 2 * set + line, -1: none.  Of partial
+// results only the kinds that can occur have places: first[3]'s, then first[2]'s, then
+// first[0]'s and first[1]'s.
 constexpr int kKinds = 4;
 struct AttendSession {
   int32_t status, n, t0;  // rows in use, their first place in row_of
@@ -92,10 +96,14 @@ inline int wide_rows(int head_dim) { return 64 * wide_tiles(head_dim); }
 __host__ __device__ inline int worth(int n_kv, int head_dim, int n) {
   return 180000000 / (n_kv * head_dim * (n < 20 ? 20 : n > 140 ? 140 : n));
 }
-// Whether a plan can hold wide sets: rows too many for a narrow one, or B sessions of
-// `most` tokens that can share enough.  Where it cannot, their kernel is not launched.
+// Whether B sessions of `most` tokens can share enough.
+inline bool may_share(int n_kv, int head_dim, int B, int64_t most) {
+  return B > 1 && most >= worth(n_kv, head_dim, B);
+}
+// Whether a plan can hold wide sets: rows too many for a narrow one, or shared keys.
+// Where it cannot, their kernel is not launched.
 inline bool may_be_wide(int64_t rows, int n_kv, int head_dim, int B, int64_t most) {
-  return rows > narrow_rows(rows, head_dim) || (B > 1 && most >= worth(n_kv, head_dim, B));
+  return rows > narrow_rows(rows, head_dim) || may_share(n_kv, head_dim, B, most);
 }
 
 struct PlanSizes {

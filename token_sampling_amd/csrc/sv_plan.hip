@@ -85,6 +85,7 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
   __shared__ int64_t smem[kOne / kWave];
   const CacheView& c = a.c;
   const int tid = threadIdx.x;
+  const int many = (int64_t)a.R * a.G > a.narrow;  // whether sets of the third kind can occur
   int st[kPer], n[kPer], len[kPer], slot[kPer], run[2][kPer], shared[kPer];
 
   // the sessions' rows
@@ -240,7 +241,8 @@ __global__ __launch_bounds__(kOne) void k_plan(PlanArgs a) {
           AttendSet* sets = cc.line ? a.p.sets[1] : a.p.sets[0];
           for (int q = 0; q < cc.n; ++q, ++at, y += nb)
             sets[at] = AttendSet{t_at[b], q * cc.per, min(cc.per, rows - q * cc.per), from,
-                                 key[k][i], list, k < 3 ? kFar : len[i], k == 3 && from == 0, y, cc.per, 0};
+                                 key[k][i], list, k < 3 ? kFar : len[i], k == 3 && from == 0, y, cc.per,
+                                 k < 2 ? many + 1 + k : 3 - k};
           if (cc.line) s[1] = at, x[1] = y;
           else s[0] = at, x[0] = y;
         } else {
