@@ -708,7 +708,7 @@ int sv_cache_plan(const sv_cache *cache, const int32_t *slots, const int32_t *ro
  * contiguous, not overlapping q or the cache.  Rows that a session does not use are neither read nor
  * written; all R rows of a failed session become NaN.  scale > 0, and
  * finite times log2(e) in binary32.
- * plan: of sv_cache_plan with the same cache, n_heads, B and R.  workspace:
+ * plan: of sv_cache_plan with the same lists, n_heads, B and R.  workspace:
  * sv_cache_attention_bytes(), 16-byte aligned; calls that overlap need distinct
  * ones.  It holds B * R * n_heads partial results of 4 * (head_dim + 2) bytes: one
  * each; one more where R * n_heads / n_kv > 64 (16 for a head_dim of 256); two more

@@ -35,3 +35,20 @@ def test_out_in_the_cache(plane):
         out = pool.view(-1)[begin:begin + n].view(q.shape)
         out.fill_(7)
         assert not sv.cache_attention(cache, 0, q, plan, out=out).any()
+
+
+@pytest.mark.parametrize("other", [dict(page=64, max_pages=4), dict(n_slots=3), dict(max_pages=7)])
+def test_plan_of_another_cache(other):
+    """A plan names slots and places in their lists: of a cache with fewer or shorter ones it would
+    lead behind the table."""
+    sizes = dict(n_slots=5, n_pages=20, max_pages=8, n_kv=2, head_dim=64, page=32)
+    cache, wrong = sv.make_cache(**sizes), sv.make_cache(**{**sizes, **other})
+    assert not sv.cache_reserve(cache, torch.full((2,), 200, dtype=torch.int32, device="cuda")).any()
+    plan = sv.cache_plan(cache, 4, 1, B=2)
+    q = torch.zeros((2, 1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="plan is of a cache of other pages"):
+        sv.cache_attention(wrong, 0, q, plan)
+    for x in cache[:2]:
+        x.zero_()
+    layer = cache._replace(k=cache.k.clone(), v=cache.v.clone())  # another layer's planes, the same lists
+    assert not sv.cache_attention(layer, 0, q, plan).any()

@@ -179,7 +179,8 @@ class Cache(NamedTuple):
 class CachePlan(NamedTuple):
     """How a round's attention is split (cache_plan), for B sessions of up to R rows
     and n_heads query heads over a cache of n_kv heads of head_dim; status [B] int32;
-    workspace_bytes: what cache_attention needs."""
+    workspace_bytes: what cache_attention needs; lists: the cache's page, n_slots and
+    max_pages, which say where its lists of pages end."""
     buffer: "torch.Tensor"  # noqa: F821
     status: "torch.Tensor"  # noqa: F821
     n_heads: int
@@ -188,6 +189,7 @@ class CachePlan(NamedTuple):
     n_kv: int
     head_dim: int
     workspace_bytes: int
+    lists: tuple = None
 
 
 class HipEvent:
@@ -1297,7 +1299,8 @@ def cache_plan(cache, n_heads, R, rows=None, slots=None, B=None, out=None, strea
                                  buffer.data_ptr(), size, handle)
     _raise(rc, "sv_cache_plan")
     return CachePlan(buffer, status, n_heads, B, R, c.n_kv, c.head_dim,
-                     lib().sv_cache_attention_bytes(ctypes.byref(c), n_heads, B, R))
+                     lib().sv_cache_attention_bytes(ctypes.byref(c), n_heads, B, R),
+                     (c.page, c.n_slots, c.max_pages))
 
 
 def cache_attention(cache, layer, q, plan, scale=None, out=None, workspace=None, stream=None):
@@ -1316,6 +1319,8 @@ def cache_attention(cache, layer, q, plan, scale=None, out=None, workspace=None,
     scale = c.head_dim ** -0.5 if scale is None else float(scale)
     if (plan.n_kv, plan.head_dim) != (c.n_kv, c.head_dim):
         raise ValueError("plan is of a cache of other heads")
+    if plan.lists is not None and plan.lists != (c.page, c.n_slots, c.max_pages):
+        raise ValueError("plan is of a cache of other pages, slots or lists")
     p_plan = _want(plan.buffer, "plan.buffer", torch.uint8, plan.buffer.shape, dev)
     handle, on = _launch(dev, stream)
     with on:
