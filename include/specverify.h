@@ -678,18 +678,23 @@ int sv_cache_write(const sv_cache *cache, int32_t layer, const sv_rows *from, co
 
 /*
  * The plan of a round's attention: which keys and rows go together.  Where
- * neighbouring sessions (places without one between them do not count) have
- * the same leading pages, and enough of them for it to be faster (some thousand
- * tokens for few sessions, some hundred for many), these are read once for all
- * of them, on up to two levels: what a run of sessions shares, and what parts of the
- * run share beyond it; so sessions that share should be listed side by side.  The
+ * neighbouring sessions (places without one may lie between them) have the same
+ * leading pages, and enough of them for it to be faster, these are read once for
+ * all of them, on up to two levels: what a run of sessions shares, and what parts
+ * of the run share beyond it; so sessions that share should be listed side by
+ * side.  Enough for a run of n places are 1.8e8 / (n_kv * head_dim * n) tokens, n
+ * taken as 20 at least and 140 at most: with 8 heads of 128 8789 tokens for up to
+ * 20 places and 1255 from 140 on, with one head of 64 140625 and 20089.  The
  * result depends on it by the order of its sums alone.  rows [B] int32 (NULL: R): the
  * session's rows of the round.  n_heads: query heads, a multiple of n_kv.
  * plan: DEVICE, sv_cache_plan_bytes(); it holds for every layer as long as lists,
  * lengths, slots and rows stay as they are.  status: SV_S_BAD_CACHE also where the
  * rows' positions lens .. lens + rows - 1 are not all in pages that the session
  * alone holds (sv_cache_reserve did not serve it); SV_S_LIMIT: rows[b] outside
- * [0, R].  1 <= R <= SV_M_MAX + 1, n_heads <= 1024.
+ * [0, R].  1 <= R <= SV_M_MAX + 1, n_heads <= 1024.  A prompt is no round: its
+ * rows' attention is the caller's own, over the k and v that it gives to
+ * sv_cache_write; or, where a part of it is in the cache already, goes over the
+ * rest in rounds of R rows (sv_cache_reserve, _plan, _write, _attention, _keep).
  */
 size_t sv_cache_plan_bytes(const sv_cache *cache, int32_t n_heads, int32_t B, int32_t R);
 int sv_cache_plan(const sv_cache *cache, const int32_t *slots, const int32_t *rows, int32_t n_heads,
@@ -705,9 +710,9 @@ int sv_cache_plan(const sv_cache *cache, const int32_t *slots, const int32_t *ro
  * and the output once.  What a row does not see has no part in it, NaN and infinities
  * included.  q [B, R, n_heads, head_dim] of dtype at element strides q_session,
  * q_row, q_head (>= 0, multiples of 8; 16-byte aligned); out the same shape,
- * contiguous, not overlapping q or the cache.  Rows that a session does not use are neither read nor
- * written; all R rows of a failed session become NaN.  scale > 0, and
- * finite times log2(e) in binary32.
+ * contiguous, not overlapping q or the cache.  Rows that a session does not use are
+ * neither read nor written; all R rows of a failed session become NaN.  scale > 0,
+ * and finite times log2(e) in binary32.
  * plan: of sv_cache_plan with the same lists, n_heads, B and R.  workspace:
  * sv_cache_attention_bytes(), 16-byte aligned; calls that overlap need distinct
  * ones.  It holds B * R * n_heads partial results of 4 * (head_dim + 2) bytes: one

@@ -17,7 +17,7 @@ def test_attention_bytes(n_kv, dim):
     for B, R, G, pages in itertools.product((1, 2, 64, 4096), (1, 9, 65), (1, 4, 7), (1, 100, 1 << 14)):
         c = struct(n_kv=n_kv, head_dim=dim, max_pages=pages, n_slots=4096)
         many = R * G > (16 if dim == 256 else 64)
-        share = B > 1 and pages * 64 >= 180000000 // (n_kv * dim * min(max(B, 16), 140))
+        share = B > 1 and pages * 64 >= 180000000 // (n_kv * dim * min(max(B, 20), 140))
         places = (1 + many + 2 * share) * B * R * G * n_kv + 512 * (64 + 192 * (many or share))
         got = sv.lib().sv_cache_attention_bytes(c, n_kv * G, B, R)
         assert 4 * (dim + 2) * B * R * G * n_kv < got <= 4 * (dim + 2) * places

@@ -72,9 +72,10 @@ struct AttendPlan {
 
 // Rows of a narrow set at most, by the rows that a round brings a key head, and of a
 // wide one.  Up to 64 rows a session's keys go into one narrow set, all of whose rows
-// have to fit a wave's registers: 64 sessions of 8192 tokens, 8 heads of 128, 64 rows,
-// take 465 us so and 497 as wide sets (heads of 64: 251 and 349), 68 rows 457 as wide
-// sets.  What is left of a wide set's session, the keys that not all rows see, goes in
+// have to fit a wave's registers: 64 sessions of 8192 tokens, 8 heads, 64 rows, take 218
+// us so and 320 as wide sets with heads of 64, 292 and 336 with heads of 96; with heads
+// of 128 the registers spill (121 of them, 472 bytes a lane) and neither wins, 430 and
+// 420.  What is left of a wide set's session, the keys that not all rows see, goes in
 // sets of 48.  Heads of 256 leave room for 16 rows only (32 in registers: 399 against
 // 391 us for 16 rows, 449 against 446 for 32).
 inline int narrow_rows(int64_t rows, int head_dim) {
@@ -89,10 +90,21 @@ inline int wide_rows(int head_dim) { return 64 * wide_tiles(head_dim); }
 
 // Keys that n neighbours share are worth sets of their own from so many on.  Read by each
 // session they come from caches mostly, and a row's further part and the wide sets'
-// start cost some 20 us.  Measured at 8 heads of 128, a row and 9 rows a session: 4 sessions
-// break even at 6000 and 11000 keys, 16 at 13000 and 11000, 64 at 3000, 256 at 1500 and 1300
-// (of 8192 keys, 9 rows: 54 shared and 52 us unshared, 75 and 70, 149 and 197, 529
-// and 739).  Smaller heads bring fewer bytes.
+// start cost some 20 us.  Keys at which both sides were measured to take the same time, for
+// one row and for 9 rows a session, 4 query heads a key head, layers in turn; in brackets the
+// rule, which does not ask for the rows:
+//               8 heads of 128      16 of 128           8 of 64               1 of 64
+//      4        12600 9100 (8789)   2600 3700 (4394)    16300 20900 (17578)   -
+//     16        6200 5200 (8789)    3300 3000 (4394)    14300 5600 (17578)    -
+//     64        2900 3300 (2746)    1600 1800 (1373)    4900 2900 (5493)      36800 11900 (43945)
+//    256        870 1050 (1255)     <512 650 (627)      1060 <1024 (2511)     10300 3400 (20089)
+//   1024        <512 610 (1255)     <512 540 (627)      <1024 <1024 (2511)    2400 1600 (20089)
+// (8192 keys of 8 heads of 128, 9 rows: 39 us apart and 41 shared, 79 and 69, 171 and 127,
+// 659 and 415, 2667 and 1591.)  Where it is off it mostly shares too late, most so for
+// many sessions of few small heads: 1024 of one head of 64, one row, 16384 keys, take 180 us
+// where 58 would do.  n counts places, also those without a session or rows this round: 140
+// places of which 4 have rows share from 1255 keys on, where 4 would from 8789 (4 sessions
+// behind 4096 keys: 22 us shared, 17 apart).
 __host__ __device__ inline int worth(int n_kv, int head_dim, int n) {
   return 180000000 / (n_kv * head_dim * (n < 20 ? 20 : n > 140 ? 140 : n));
 }

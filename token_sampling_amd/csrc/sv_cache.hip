@@ -83,7 +83,9 @@ struct ReserveArgs {
 
 // One workgroup, kPer sessions a thread: what the sessions want, the free pages, and
 // who gets which.  13 us for 1024 sessions in a pool of 194000 pages, 8 in a small one: a
-// chain of dependent loads, and 32768 pages' refs at a time until enough are found.
+// chain of dependent loads, and 32768 pages' refs at a time until enough are found.  With
+// four sessions a thread 88 registers spill; that and k_copy without a pair take 8 us for
+// 2048 sessions that want no pages and 16 for 4096 (1024: 6).
 template <int kPer>
 __global__ __launch_bounds__(kOne) void k_reserve(ReserveArgs a) {
   __shared__ uint32_t seen[SV_CACHE_SLOTS_MAX / 32], twice[SV_CACHE_SLOTS_MAX / 32];
