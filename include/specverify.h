@@ -707,7 +707,9 @@ int sv_cache_plan(const sv_cache *cache, const int32_t *slots, const int32_t *ro
  * keys and values must be written.  Scores, weights' sums and outputs are kept
  * in binary32; a weight is rounded to dtype before it meets the values, as the
  * matrix instructions take it (half's small weights to 2^-32 of the row's largest),
- * and the output once.  What a row does not see has no part in it, NaN and infinities
+ * and the output once.  (A row may end as NaN or infinite where scores times
+ * log2(e) reach 2^28, in bfloat16 2^31: their last digit is then worth more than a
+ * weight can hold.)  What a row does not see has no part in it, NaN and infinities
  * included.  q [B, R, n_heads, head_dim] of dtype at element strides q_session,
  * q_row, q_head (>= 0, multiples of 8; 16-byte aligned); out the same shape,
  * contiguous, not overlapping q or the cache.  Rows that a session does not use are

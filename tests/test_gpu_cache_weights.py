@@ -59,3 +59,40 @@ def test_small_weights(R, dim, bits, dtype):
             if dtype == torch.float16:
                 tol += 2.0**-25 + 4096 * n_low * 2.0**-32 / n_high
             assert (np.abs(got[b, r] - want) <= tol).all(), (b, r, want, tol, np.abs(got[b, r] - want).max())
+
+
+@pytest.mark.parametrize("dim,R", [(64, 1), (128, 9), (64, 12), (96, 15), (256, 1), (64, 33), (128, 33)])
+@pytest.mark.parametrize("dtype,power", [(torch.float16, 23.2), (torch.float16, 24.4), (torch.float16, 25.7),
+                                         (torch.float16, 26.8), (torch.bfloat16, 25.7), (torch.bfloat16, 29.5)])
+def test_large_scores(dim, R, dtype, power):
+    """Scores of about 2^power, whose last binary32 digit is worth one to many powers of two, rising
+    from block to block of keys by steps of that size: outputs are means of what the keys
+    hold, never NaN or infinite.  One session listed 64 times, so that a wave has many tiles."""
+    Hkv, G, page, n, B = 8, 4, 64, 800, 64
+    cache = sv.make_cache(1, 14, 14, Hkv, dim, page=page, dtype=dtype)
+    rng = np.random.default_rng(R)
+    ref = filled(cache, rng, [n + R])
+    as_bits = lambda x: torch.from_numpy(np.asarray(x)).to(dtype).view(torch.int16).numpy()  # noqa: E731
+    # half the dimensions make the scores' size, one the steps, which differ from row to row
+    size = 2.0**power / np.log2(np.e) / (dim // 2)
+    side = 2.0**np.floor(np.log2(size) / 2)
+    k, q = np.zeros(dim), np.zeros((B, R, Hkv * G, dim))
+    k[:dim // 2] = side
+    q[..., :dim // 2] = size / side * rng.uniform(0.9, 1.1, (B, R, Hkv * G, 1))
+    q[..., dim - 1] = rng.integers(2, 15, (B, R, Hkv * G))
+    for t in range(n + R):
+        p, u = ref.table[0, t // page], t % page
+        k[dim - 1] = t // 128
+        ref.k[0, p, :, u] = as_bits(k)
+        ref.v[0, p, :, u] = as_bits(np.full(dim, 1.0 + t // 128))
+    ref.lens[:] = n
+    ref.store()
+    slots = dev([0] * B)
+    plan = sv.cache_plan(cache, Hkv * G, R, slots=slots)
+    got = sv.cache_attention(cache, 0, torch.from_numpy(q).to(dtype).cuda(), plan, scale=1.0)
+    assert not plan.status.any()
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all()
+    # between the smallest and the largest value, with the weights', the output's and the sums' roundings
+    slack = 1 + 2 * torch.finfo(dtype).eps / 2 + (n + R + 4) * 2.0**-23
+    assert (got >= 1 / slack).all() and (got <= (1 + (n + R) // 128) * slack).all()

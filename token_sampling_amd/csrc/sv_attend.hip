@@ -131,7 +131,11 @@ __device__ inline void score(const u32x4 (&kf)[kC], const u32x4 (&q)[kC], f32x4&
 // bfloat16, whose exponents reach far enough with a kLift of 0.  Halves end at 2^16 and
 // have fewer digits below 2^-14, so kLift is 7 there: a key's weight is off by half its last
 // digit or 2^-32 of the largest, and 131072 keys together by 2^-15 at most (without the
-// lift 2^-25 and 2^-8: they would be lost from the values but not from the sum).
+// lift 2^-25 and 2^-8: they would be lost from the values but not from the sum).  Whether m
+// has to follow is asked of the weight's own exponent, rounded as the weight's is: z * scale
+// and m + kReach are rounded otherwise, and from scores of 2^24 on, whose last digit is
+// worth 2, a weight would pass 2^16 unnoticed.  m itself is off by half its last digit,
+// which is harmless up to scores of 2^28 (bfloat16 2^31).
 constexpr float kSlack = 8.0f;
 template <typename E>
 constexpr float kReach = E::kLift + kSlack;
@@ -151,17 +155,17 @@ __device__ inline bool look_up(f32x4 (&z)[NT][2], float (&top)[NT], float scale,
     top[t] = z[t][0][0];
 #pragma unroll
     for (int e = 1; e < 8; ++e) top[t] = fmaxf(top[t], z[t][e / 4][e % 4]);
-    top[t] *= scale;
-    far |= top[t] > m[t] + kReach<E>;
+    far |= fmaf(top[t], scale, -m[t]) > kReach<E>;
   }
   return __any(far);
 }
 template <typename E, int NT, int kN>
-__device__ inline void follow(const float (&top)[NT], float (&m)[NT], float (&l)[NT], f32x4 (&o)[NT][kN]) {
+__device__ inline void follow(const float (&top)[NT], float scale, float (&m)[NT], float (&l)[NT],
+                              f32x4 (&o)[NT][kN]) {
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float now = fmaxf(top[t], lane_xor<16>(top[t]));
-    now = fmaxf(m[t], fmaxf(now, lane_xor<32>(now)) - E::kLift);
+    now = fmaxf(m[t], fmaf(fmaxf(now, lane_xor<32>(now)), scale, -E::kLift));
     const float keep = __builtin_amdgcn_exp2f(m[t] - now);
     m[t] = now;
     l[t] *= keep;
@@ -190,7 +194,7 @@ template <typename E, bool kEdge, int NT, int kN>
 __device__ inline void weigh(f32x4 (&z)[NT][2], u32x4 (&w)[NT], float scale, int key, const int (&lim)[NT],
                              float (&m)[NT], float (&l)[NT], f32x4 (&o)[NT][kN]) {
   float top[NT], sum[NT];
-  if (look_up<E, kEdge>(z, top, scale, key, lim, m)) follow<E>(top, m, l, o);
+  if (look_up<E, kEdge>(z, top, scale, key, lim, m)) follow<E>(top, scale, m, l, o);
   powers<E>(z, w, sum, scale, m);
 #pragma unroll
   for (int t = 0; t < NT; ++t) l[t] += sum[t];
@@ -553,7 +557,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void k_attend_wide(Atten
     bool far = true;
     for (int i = 0;;) {
       if (far) {
-        follow<E>(top, m, l, o);
+        follow<E>(top, a.scale, m, l, o);
         powers<E>(z, w, sum, a.scale, m);
       }
       if (i + 1 == tiles) break;
@@ -565,7 +569,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void k_attend_wide(Atten
         in_turn<E>(&tile[(i + 1) % kRing][0], &tile[i % kRing][2 * kC], q, w, o, z, top, sum, a.scale, m);
         far = false;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) far |= (top[t] *= a.scale) > m[t] + kReach<E>;
+        for (int t = 0; t < NT; ++t) far |= fmaf(top[t], a.scale, -m[t]) > kReach<E>;
         far = __any(far);
         ++i;
       } while (!far && i + 1 < tiles);

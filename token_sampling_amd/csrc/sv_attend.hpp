@@ -74,7 +74,7 @@ struct AttendPlan {
 // wide one.  Up to 64 rows a session's keys go into one narrow set, all of whose rows
 // have to fit a wave's registers: 64 sessions of 8192 tokens, 8 heads, 64 rows, take 218
 // us so and 320 as wide sets with heads of 64, 292 and 336 with heads of 96; with heads
-// of 128 the registers spill (121 of them, 472 bytes a lane) and neither wins, 430 and
+// of 128 the registers spill (133 of them, 472 bytes a lane) and neither wins, 430 and
 // 420.  What is left of a wide set's session, the keys that not all rows see, goes in
 // sets of 48.  Heads of 256 leave room for 16 rows only (32 in registers: 399 against
 // 391 us for 16 rows, 449 against 446 for 32).
